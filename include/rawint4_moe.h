@@ -325,6 +325,119 @@ RAWINT4_API int rawint4_moe_router_bwd(const float* scores, int32_t qlen, int32_
                                        const int64_t* ids, const float* grad_route, const float* escale,
                                        float* grad_scores, float* grad_escale, void* stream);
 
+/* ------------------------------------------------- around the layer
+ * What stands in front of the layer in a training or serving step: the norm
+ * of the token rows, the selection of experts from router scores, and the
+ * token rows kept in 8 bits between forward and backward. No counterpart in
+ * the method, which starts at expert ids and weights. All calls follow the
+ * conventions at the top; `ld*` are row pitches in elements (>= the width,
+ * <= 2^28), rows themselves are dense. Rows whose start is 16-byte aligned
+ * and whose width is a multiple of 8 move with vector accesses; every other
+ * alignment and width is served too, element by element. An output must not
+ * overlap an input (RAWINT4_INVALID_ARGUMENT where the call can see it). */
+enum { RAWINT4_TYPE_F32 = 0, RAWINT4_TYPE_BF16 = 1, RAWINT4_TYPE_F16 = 2 }; /* element types */
+
+/* Expert selection, beside rawint4_moe_router_topk: p = softmax(scores) over
+ * all experts or sigmoid(scores); key = p + bias. With groups > 1 the experts
+ * lie in `groups` equal runs; a group's score is the sum of its group_top
+ * largest keys (experts scored -inf are left out unless nothing else remains),
+ * and only the groups_kept groups of largest score stay in. The top_k experts
+ * of largest key are selected, largest first; equal keys, and equal groups, go
+ * to the lower index. Keys are compared as the real numbers they stand for,
+ * not as their fp32 roundings. weights = scale * p_i / (sum of the k p) when
+ * renormalise is nonzero, else scale * p_i; the bias only ranks.
+ * A score of -inf or NaN has p = 0 and ranks behind every other score: a token
+ * with fewer than k other scores gets the lowest such indices with weight 0. A
+ * bias of -inf or NaN ranks the expert last as well and leaves its weight.
+ * Limits: experts <= 4096, top_k <= 32, groups <= 32, experts % groups == 0,
+ * 1 <= groups_kept <= groups, group_top 1 or 2 (at most experts / groups),
+ * top_k <= groups_kept * experts / groups, scale finite. */
+enum { RAWINT4_SCORE_SOFTMAX = 0, RAWINT4_SCORE_SIGMOID = 1 };
+typedef struct rawint4_moe_select_cfg {
+  int32_t experts, top_k;
+  int32_t groups, groups_kept, group_top; /* 1, 1, 1: no groups */
+  int32_t score;                          /* RAWINT4_SCORE_* */
+  int32_t renormalise;
+  int32_t type; /* RAWINT4_TYPE_* of scores and grad_scores */
+  float scale;
+} rawint4_moe_select_cfg;
+
+/* scores [Q, E] of cfg->type (pitch ld), bias fp32 [E] (may be NULL: 0) ->
+ * ids int64 [Q, k], weights fp32 [Q, k] (the layer's inputs), counts int32 [E]
+ * (may be NULL; overwritten): slots routed to each expert, for the caller's
+ * update of the bias. All device pointers. */
+RAWINT4_API int rawint4_moe_router_select(const rawint4_moe_select_cfg* cfg, const void* scores, int64_t ld, int32_t qlen,
+                                          const float* bias, int64_t* ids, float* weights, int32_t* counts,
+                                          void* stream);
+/* grad_scores [Q, E] of cfg->type (dense, overwritten) = dL/dscores from
+ * grad_route fp32 [Q, k] = dL/dweights, for the ids that a selection returned.
+ * An id outside [0, E) contributes nothing; slots that name the same expert
+ * add up. The selection itself is constant: no gradient reaches the bias. */
+RAWINT4_API int rawint4_moe_router_select_bwd(const rawint4_moe_select_cfg* cfg, const void* scores, int64_t ld,
+                                              int32_t qlen, const int64_t* ids, const float* grad_route,
+                                              void* grad_scores, void* stream);
+
+/* Activation checkpoints in 8 bits. 32 neighbours of a row (fewer at its end)
+ * share the scale 2^e, kept as the byte e + 127 like the UE8M0 scales of the
+ * MXFP4 base: e is the smallest exponent >= -126 under which the group's
+ * largest finite magnitude is at most 448 (E4M3) or below 127.5 (INT8), so no
+ * value is clipped and x * 2^-e is exact. code = that value rounded once, to
+ * nearest, ties to even: an E4M3 number, or a two's complement integer in
+ * [-127, 127]. Values that are not finite come back as NaN (codes 0x7f and
+ * 0x80); a finite value comes back finite, at most the type's largest number.
+ *   x / out [rows, width] fp32, bf16 or fp16 (out dense),
+ *   codes uint8 [rows, width], scales uint8 [rows, ceil(width / 32)], dense.
+ * Limits: rows < 2^31, 1 <= width <= 2^20. */
+enum { RAWINT4_CKPT_E4M3 = 0, RAWINT4_CKPT_INT8 = 1 };
+typedef struct rawint4_ckpt8 {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int32_t format; /* RAWINT4_CKPT_* */
+} rawint4_ckpt8;
+RAWINT4_API int rawint4_ckpt8_save(int32_t format, int32_t type, const void* x, int64_t ldx, int64_t rows, int32_t width,
+                                   uint8_t* codes, uint8_t* scales, void* stream);
+RAWINT4_API int rawint4_ckpt8_load(int32_t format, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                   int32_t width, int32_t type, void* out, void* stream);
+
+/* Layer norm and RMS norm of rows: with mu the row mean (RMS: 0) and
+ * r = 1 / sqrt(mean((x - mu)^2) + eps), y = (x - mu) r w + b. Statistics and
+ * sums in fp32, each output rounded once.
+ * Limits: 1 <= width <= 16384, rows >= 0, eps > 0 and finite. */
+enum { RAWINT4_NORM_LAYER = 0, RAWINT4_NORM_RMS = 1 };
+typedef struct rawint4_norm_cfg {
+  int32_t rows, width;
+  int32_t kind;        /* RAWINT4_NORM_* */
+  int32_t type;        /* RAWINT4_TYPE_* of x, y and their gradients */
+  int32_t weight_type; /* RAWINT4_TYPE_* of weight, bias and their gradients */
+  float eps;
+} rawint4_norm_cfg;
+
+/* Forward. The input is x [rows, width] (pitch ldx), or, when x is NULL, the
+ * checkpoint x_ckpt (host struct of device pointers), whose values are used as
+ * they were saved.
+ *   weight, bias  [width], each may be NULL (1 and 0)
+ *   y             [rows, width] dense
+ *   mean, rstd    fp32 [rows], for the backward (mean NULL for RMS)
+ *   save_codes, save_scales  both or neither: x's checkpoint in save_format,
+ *                 written in the same pass (x only, not a checkpoint) */
+RAWINT4_API int rawint4_norm_fwd(const rawint4_norm_cfg* cfg, const void* x, int64_t ldx, const rawint4_ckpt8* x_ckpt,
+                                 const void* weight, const void* bias, void* y, float* mean, float* rstd,
+                                 int32_t save_format, uint8_t* save_codes, uint8_t* save_scales, void* stream);
+
+/* Backward from x or its checkpoint, with the forward's mean (NULL for RMS)
+ * and rstd:
+ *   xh = (x - mean) rstd, grad_x = rstd (w dy - mean(w dy) - xh mean(w dy xh))
+ *   (RMS: without the middle term), grad_weight = (accumulate ? grad_weight :
+ *   0) + sum over rows of dy xh, grad_bias the same of dy; both may be NULL.
+ * The sums are added in an order that depends on the shape alone. workspace:
+ * device scratch of rawint4_norm_bwd_workspace_size bytes, 16-byte aligned
+ * (may be NULL when both weight gradients are). */
+RAWINT4_API int rawint4_norm_bwd_workspace_size(const rawint4_norm_cfg* cfg, size_t* bytes);
+RAWINT4_API int rawint4_norm_bwd(const rawint4_norm_cfg* cfg, const void* x, int64_t ldx, const rawint4_ckpt8* x_ckpt,
+                                 const void* grad_y, int64_t ldg, const void* weight, const float* mean,
+                                 const float* rstd, void* grad_x, void* grad_weight, void* grad_bias, int accumulate,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
 /* Test export (no counterpart in the method): the saved forward context of
  * `workspace` (left by the most recent saving rawint4_moe_lora_fwd and not yet
  * consumed by a backward), copied into caller-owned device buffers:

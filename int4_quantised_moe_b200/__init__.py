@@ -11,6 +11,7 @@ _EXPORTS = (
     "Layer", "RawInt4Error", "FrozenBaseError", "library", "make_base", "make_cfg", "make_grads", "make_lora",
     "rawint4_decode", "rawint4_moe_lora_bwd", "rawint4_moe_lora_fwd", "rawint4_moe_lora_status",
     "rawint4_moe_lora_workspace_size", "rawint4_moe_permute", "strerror", "profile_begin", "profile_end",
+    "Ckpt8", "ckpt8_load", "ckpt8_save", "make_select_cfg", "norm_bwd", "norm_fwd", "router_select", "router_select_bwd",
 )
 
 

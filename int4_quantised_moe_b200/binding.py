@@ -54,6 +54,13 @@ EXPORTED_SYMBOLS = (
     "rawint4_moe_dispatch_rows",
     "rawint4_moe_combine_slots",
     "rawint4_moe_gather_slots",
+    "rawint4_moe_router_select",
+    "rawint4_moe_router_select_bwd",
+    "rawint4_ckpt8_save",
+    "rawint4_ckpt8_load",
+    "rawint4_norm_fwd",
+    "rawint4_norm_bwd_workspace_size",
+    "rawint4_norm_bwd",
 )
 
 
@@ -73,6 +80,20 @@ class Lora(ctypes.Structure):
 
 class LoraGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("gate_a", "gate_b", "up_a", "up_b", "down_a", "down_b")]
+
+
+class SelectCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("experts", "top_k", "groups", "groups_kept", "group_top", "score",
+                                              "renormalise", "type")] + [("scale", ctypes.c_float)]
+
+
+class Ckpt8Ptrs(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int32)]
+
+
+class NormCfg(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("kind", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("weight_type", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class RawInt4Error(RuntimeError):
@@ -113,6 +134,14 @@ def _load() -> ctypes.CDLL:
     lib.rawint4_moe_dispatch_rows.argtypes = [vp, vp, i32, i32, i32, vp, vp]
     lib.rawint4_moe_combine_slots.argtypes = [vp, vp, i32, i32, i32, vp, vp]
     lib.rawint4_moe_gather_slots.argtypes = [vp, vp, i32, vp, vp]
+    lib.rawint4_moe_router_select.argtypes = [P(SelectCfg), vp, i64, i32, vp, vp, vp, vp, vp]
+    lib.rawint4_moe_router_select_bwd.argtypes = [P(SelectCfg), vp, i64, i32, vp, vp, vp, vp]
+    lib.rawint4_ckpt8_save.argtypes = [i32, i32, vp, i64, i64, i32, vp, vp, vp]
+    lib.rawint4_ckpt8_load.argtypes = [i32, vp, vp, i64, i32, i32, vp, vp]
+    lib.rawint4_norm_fwd.argtypes = [P(NormCfg), vp, i64, P(Ckpt8Ptrs), vp, vp, vp, vp, vp, i32, vp, vp, vp]
+    lib.rawint4_norm_bwd_workspace_size.argtypes = [P(NormCfg), P(sz)]
+    lib.rawint4_norm_bwd.argtypes = [P(NormCfg), vp, i64, P(Ckpt8Ptrs), vp, i64, vp, vp, vp, vp, vp, vp, ctypes.c_int,
+                                     vp, sz, vp]
     for name in EXPORTED_SYMBOLS:
         if name != "rawint4_moe_lora_strerror":
             getattr(lib, name).restype = ctypes.c_int  # raises AttributeError if the library lacks it
@@ -442,6 +471,295 @@ def router_bwd(scores: torch.Tensor, ids: torch.Tensor, grad_route: torch.Tensor
     _check(_lib.rawint4_moe_router_bwd(_ptr(scores), q, E, k, _ptr(ids), _ptr(grad_route), _ptr(escale), _ptr(dz),
                                        _ptr(dc), _stream(stream)), "rawint4_moe_router_bwd")
     return (dz, dc) if want_escale_grad else dz
+
+
+# ---------------------------------------------------------------------------
+# Around the layer: expert selection, 8-bit activation checkpoints, norm
+# ---------------------------------------------------------------------------
+# Every call runs on the device of its tensors. `stream` defaults to that
+# device's current stream; results and scratch are allocated on the stream
+# that the call runs on.
+
+TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+CKPT_FORMATS = {"e4m3": 0, "int8": 1}
+NORM_KINDS = {"layer": 0, "rms": 1}
+CKPT_GROUP = 32  # columns under one scale of a checkpoint
+
+
+class _On:
+    """The device and stream of a call: enters the tensors' device, and the given stream when there
+    is one, so that torch allocates there; yields the raw stream handle."""
+
+    __slots__ = ("device", "stream", "guards")
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream, self.guards = device, stream, ()
+
+    def __enter__(self) -> int:
+        index = self.device.index
+        if self.stream is None:
+            if index != torch.cuda.current_device():
+                guard = torch.cuda.device(index)
+                guard.__enter__()
+                self.guards = (guard,)
+            return torch.cuda.current_stream(index).cuda_stream
+        s = self.stream
+        if not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(s), device=self.device)
+        if s.device != self.device:
+            raise ValueError(f"the stream is on {s.device}, the tensors are on {self.device}")
+        guard = torch.cuda.stream(s)
+        guard.__enter__()
+        self.guards = (guard,)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        for g in self.guards:
+            g.__exit__(*exc)
+        return False
+
+
+def _choice(table: dict, value, name: str) -> int:
+    code = table.get(value)
+    if code is None:
+        raise ValueError(f"{name}: expected one of {sorted(map(str, table))}, got {value!r}")
+    return code
+
+
+def _rows(t, name: str, width: Optional[int] = None, device: Optional[torch.device] = None, dtype=None) -> int:
+    """Checks a [rows, width] CUDA tensor of fp32, bf16 or fp16 whose rows are dense (any row pitch of
+    at least the width); returns the pitch."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in TYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name}: expected dtype {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 2 or (width is not None and shape[1] != width):
+        raise ValueError(f"{name}: expected shape [rows, {'width' if width is None else width}], got {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+    pitch, inner = t.stride()
+    if shape[0] <= 1:
+        pitch = shape[1]  # torch leaves the pitch of a single row open
+    if (inner != 1 and shape[1] > 1) or pitch < shape[1]:
+        raise ValueError(f"{name}: expected dense rows (strides (pitch >= width, 1)), got strides {t.stride()}")
+    return pitch
+
+
+def make_select_cfg(experts: int, top_k: int, score: str = "sigmoid", groups: int = 1, groups_kept: Optional[int] = None,
+                    group_top: int = 1, renormalise: bool = True, scale: float = 1.0) -> SelectCfg:
+    """Configuration of router_select: `score` "sigmoid" or "softmax"; `groups` equal runs of experts of
+    which the groups_kept (default: all) of largest score, the sum of their group_top best keys, stay in."""
+    return SelectCfg(int(experts), int(top_k), int(groups), int(groups if groups_kept is None else groups_kept),
+                     int(group_top), _choice(SCORES, score, "score"), 1 if renormalise else 0, 0, float(scale))
+
+
+def _typed(cfg: SelectCfg, dtype: torch.dtype) -> SelectCfg:
+    return SelectCfg(cfg.experts, cfg.top_k, cfg.groups, cfg.groups_kept, cfg.group_top, cfg.score, cfg.renormalise,
+                     TYPES[dtype], cfg.scale)
+
+
+def router_select(scores: torch.Tensor, cfg: SelectCfg, bias: Optional[torch.Tensor] = None,
+                  counts: Optional[torch.Tensor] = None, stream=None):
+    """Expert ids int64 [Q, k] and route weights fp32 [Q, k] from router scores [Q, E] (fp32, bf16 or
+    fp16): sigmoid or softmax, a balance bias fp32 [E] that ranks only, groups, top-k, optionally
+    renormalised, times cfg.scale. `counts` int32 [E] (optional, overwritten) receives the slots routed
+    to each expert."""
+    E = cfg.experts
+    pitch = _rows(scores, "scores", E)
+    dev = scores.device
+    if bias is not None:
+        _expect(bias, "bias", torch.float32, (E,), dev)
+    if counts is not None:
+        _expect(counts, "counts", torch.int32, (E,), dev)
+    q = scores.shape[0]
+    with _On(dev, stream) as st:
+        ids = torch.empty((q, cfg.top_k), dtype=torch.int64, device=dev)
+        w = torch.empty((q, cfg.top_k), dtype=torch.float32, device=dev)
+        _check(_lib.rawint4_moe_router_select(_typed(cfg, scores.dtype), scores.data_ptr(), pitch, q, _ptr(bias),
+                                              ids.data_ptr(), w.data_ptr(), _ptr(counts), st),
+               "rawint4_moe_router_select")
+    return ids, w
+
+
+def router_select_bwd(scores: torch.Tensor, cfg: SelectCfg, ids: torch.Tensor, grad_route: torch.Tensor,
+                      stream=None) -> torch.Tensor:
+    """dL/dscores [Q, E] in the scores' type from the layer's grad_route fp32 [Q, k]."""
+    pitch = _rows(scores, "scores", cfg.experts)
+    dev = scores.device
+    q = scores.shape[0]
+    _expect(ids, "ids", torch.int64, (q, cfg.top_k), dev)
+    _expect(grad_route, "grad_route", torch.float32, (q, cfg.top_k), dev)
+    with _On(dev, stream) as st:
+        grad = torch.empty((q, cfg.experts), dtype=scores.dtype, device=dev)
+        _check(_lib.rawint4_moe_router_select_bwd(_typed(cfg, scores.dtype), scores.data_ptr(), pitch, q, ids.data_ptr(),
+                                                  grad_route.data_ptr(), grad.data_ptr(), st),
+               "rawint4_moe_router_select_bwd")
+    return grad
+
+
+@dataclass
+class Ckpt8:
+    """Rows kept in 8 bits: codes uint8 [rows, width], one scale byte per 32 columns uint8
+    [rows, ceil(width / 32)], format "e4m3" or "int8"."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    format: str
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+    def check(self, name: str, device: Optional[torch.device] = None) -> int:
+        """Raises unless the tensors fit together; returns the format's number."""
+        fmt = _choice(CKPT_FORMATS, self.format, f"{name}.format")
+        codes = self.codes
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+            raise ValueError(f"{name}.codes: expected a uint8 tensor [rows, width]")
+        rows, width = codes.shape
+        _expect(codes, f"{name}.codes", torch.uint8, (rows, width), device)
+        _expect(self.scales, f"{name}.scales", torch.uint8, (rows, -(-width // CKPT_GROUP)), codes.device)
+        return fmt
+
+
+def _empty_ckpt8(rows: int, width: int, fmt: str, device) -> Ckpt8:
+    return Ckpt8(torch.empty((rows, width), dtype=torch.uint8, device=device),
+                 torch.empty((rows, -(-width // CKPT_GROUP)), dtype=torch.uint8, device=device), fmt)
+
+
+def ckpt8_save(x: torch.Tensor, format: str = "e4m3", stream=None) -> Ckpt8:
+    """x [rows, width] (fp32, bf16 or fp16) in 8 bits; see include/rawint4_moe.h for the format."""
+    fmt = _choice(CKPT_FORMATS, format, "format")
+    pitch = _rows(x, "x")
+    rows, width = x.shape
+    with _On(x.device, stream) as st:
+        out = _empty_ckpt8(rows, width, format, x.device)
+        _check(_lib.rawint4_ckpt8_save(fmt, TYPES[x.dtype], x.data_ptr(), pitch, rows, width, out.codes.data_ptr(),
+                                       out.scales.data_ptr(), st), "rawint4_ckpt8_save")
+    return out
+
+
+def ckpt8_load(ckpt: Ckpt8, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The rows of a checkpoint, [rows, width] in `dtype`."""
+    fmt = ckpt.check("ckpt")
+    typ = _choice(TYPES, dtype, "dtype")
+    codes = ckpt.codes
+    rows, width = codes.shape
+    with _On(codes.device, stream) as st:
+        out = torch.empty((rows, width), dtype=dtype, device=codes.device)
+        _check(_lib.rawint4_ckpt8_load(fmt, codes.data_ptr(), ckpt.scales.data_ptr(), rows, width, typ, out.data_ptr(),
+                                       st), "rawint4_ckpt8_load")
+    return out
+
+
+def _norm_input(x, name: str):
+    """(rows, width, device, pointer, pitch, checkpoint pointers) of a norm's input."""
+    if isinstance(x, Ckpt8):
+        fmt = x.check(name)
+        rows, width = x.codes.shape
+        return rows, width, x.codes.device, None, 0, Ckpt8Ptrs(x.codes.data_ptr(), x.scales.data_ptr(), fmt)
+    pitch = _rows(x, name)
+    return x.shape[0], x.shape[1], x.device, x.data_ptr(), pitch, None
+
+
+def _vector(t, name: str, width: int, device: torch.device) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype not in TYPES:
+        raise TypeError(f"{name}: expected a float32, bfloat16 or float16 tensor")
+    _expect(t, name, t.dtype, (width,), device)
+
+
+def norm_fwd(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, kind: str = "rms",
+             eps: float = 1e-6, dtype: Optional[torch.dtype] = None, save: Optional[str] = None, stream=None):
+    """Layer or RMS norm of the rows of x, a tensor [rows, width] or a Ckpt8 (then `dtype` is the
+    result's type, bf16 by default). Returns (y, mean, rstd, ckpt): mean is None for kind "rms", ckpt is
+    x in 8 bits when `save` names a format, else None."""
+    rows, width, dev, ptr, pitch, ck = _norm_input(x, "x")
+    k = _choice(NORM_KINDS, kind, "kind")
+    if ck is None:
+        if dtype is not None and dtype != x.dtype:
+            raise TypeError(f"dtype: a tensor's norm has its type {x.dtype}, got {dtype}")
+        dtype = x.dtype
+    elif save is not None:
+        raise ValueError("save: the input is a checkpoint already")
+    elif dtype is None:
+        dtype = torch.bfloat16
+    typ = _choice(TYPES, dtype, "dtype")
+    fmt = 0 if save is None else _choice(CKPT_FORMATS, save, "save")
+    wdtype = dtype
+    if weight is not None:
+        _vector(weight, "weight", width, dev)
+        wdtype = weight.dtype
+    if bias is not None:
+        if weight is None:
+            wdtype = bias.dtype
+        _vector(bias, "bias", width, dev)
+        _expect(bias, "bias", wdtype, (width,), dev)
+    with _On(dev, stream) as st:
+        y = torch.empty((rows, width), dtype=dtype, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        mean = torch.empty(rows, dtype=torch.float32, device=dev) if kind == "layer" else None
+        out = None if save is None else _empty_ckpt8(rows, width, save, dev)
+        _check(_lib.rawint4_norm_fwd(NormCfg(rows, width, k, typ, TYPES[wdtype], eps), ptr, pitch, ck, _ptr(weight),
+                                     _ptr(bias), y.data_ptr(), _ptr(mean), rstd.data_ptr(), fmt,
+                                     None if out is None else out.codes.data_ptr(),
+                                     None if out is None else out.scales.data_ptr(), st), "rawint4_norm_fwd")
+    return y, mean, rstd, out
+
+
+def norm_bwd(grad_y: torch.Tensor, x, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
+             mean: Optional[torch.Tensor] = None, kind: str = "rms", bias_grad: bool = False,
+             grad_weight: Optional[torch.Tensor] = None, grad_bias: Optional[torch.Tensor] = None,
+             accumulate: bool = False, stream=None):
+    """Backward of norm_fwd from its input x (a tensor, or the Ckpt8 kept in its place) and statistics.
+    Returns (grad_x, grad_weight, grad_bias) in the types of grad_y and of the weight; grad_weight is None
+    without a weight, grad_bias unless it is asked for. Buffers may be given; accumulate=True adds to them."""
+    rows, width, dev, ptr, pitch, ck = _norm_input(x, "x")
+    k = _choice(NORM_KINDS, kind, "kind")
+    gpitch = _rows(grad_y, "grad_y", width, dev, None if ck is not None else x.dtype)
+    if grad_y.shape[0] != rows:
+        raise ValueError(f"grad_y: expected {rows} rows, got {grad_y.shape[0]}")
+    _expect(rstd, "rstd", torch.float32, (rows,), dev)
+    if kind == "layer":
+        _expect(mean, "mean", torch.float32, (rows,), dev)
+    elif mean is not None:
+        raise ValueError("mean: the RMS norm has none")
+    dtype = grad_y.dtype
+    wdtype = dtype
+    if weight is not None:
+        _vector(weight, "weight", width, dev)
+        wdtype = weight.dtype
+    elif grad_weight is not None:
+        raise ValueError("grad_weight: the norm has no weight")
+    elif grad_bias is not None:
+        _vector(grad_bias, "grad_bias", width, dev)
+        wdtype = grad_bias.dtype
+    if accumulate and ((weight is not None and grad_weight is None) or (bias_grad and grad_bias is None)):
+        raise ValueError("accumulate: needs the buffers to add to")
+    if grad_weight is not None:
+        _expect(grad_weight, "grad_weight", wdtype, (width,), dev)
+    if grad_bias is not None:
+        _expect(grad_bias, "grad_bias", wdtype, (width,), dev)
+    with _On(dev, stream) as st:
+        grad_x = torch.empty((rows, width), dtype=dtype, device=dev)
+        if weight is not None and grad_weight is None:
+            grad_weight = torch.empty(width, dtype=wdtype, device=dev)
+        if bias_grad and grad_bias is None:
+            grad_bias = torch.empty(width, dtype=wdtype, device=dev)
+        cfg = NormCfg(rows, width, k, TYPES[dtype], TYPES[wdtype], 1.0)  # eps is in rstd already
+        ws, nbytes = None, 0
+        if grad_weight is not None or grad_bias is not None:
+            n = ctypes.c_size_t(0)
+            _check(_lib.rawint4_norm_bwd_workspace_size(cfg, n), "rawint4_norm_bwd_workspace_size")
+            nbytes = n.value
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(_lib.rawint4_norm_bwd(cfg, ptr, pitch, ck, grad_y.data_ptr(), gpitch, _ptr(weight), _ptr(mean),
+                                     rstd.data_ptr(), grad_x.data_ptr(), _ptr(grad_weight), _ptr(grad_bias),
+                                     1 if accumulate else 0, _ptr(ws), nbytes, st), "rawint4_norm_bwd")
+    return grad_x, grad_weight, grad_bias
 
 
 def set_wait_limit_ns(ns: int) -> None:

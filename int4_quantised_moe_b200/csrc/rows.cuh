@@ -1,0 +1,170 @@
+// Helpers shared by the row kernels around the layer (norm.cu, ckpt8.cu,
+// select.cu): element types, vector loads and stores, and the 8-bit
+// checkpoint code of a group of 32 values.
+//
+// Two layouts of a row over T threads:
+//   vector   thread t holds chunks t, t + T, ... of kChunk consecutive
+//            elements, moved with 16-byte accesses; needs every row to start
+//            on a 16-byte boundary and a width that is a multiple of kChunk.
+//   scalar   thread t holds elements t, t + T, ...; any width and pitch. A
+//            warp reads 32 neighbours at a time, so the accesses stay coalesced.
+#pragma once
+#include <cuda_fp8.h>
+#include <float.h>
+
+#include <initializer_list>
+
+#include "common.cuh"
+
+namespace r4 {
+
+constexpr int kChunk = 8;        // elements of one vector chunk
+constexpr int kCkptGroup = 32;   // columns under one scale of an 8-bit checkpoint
+
+template <class T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float to(float v) { return v; }
+  static __device__ __forceinline__ float from(float v) { return v; }
+  static constexpr float kMax = FLT_MAX;
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ float to(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+  static constexpr float kMax = 3.3895313892515355e38f;
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ float to(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half from(float v) { return __float2half_rn(v); }
+  static constexpr float kMax = 65504.f;
+};
+
+// One chunk as it lies in memory (16 bytes for the 16-bit types, 32 for fp32).
+template <class T>
+struct alignas(16) RawChunk {
+  T v[kChunk];
+};
+
+template <class T>
+__device__ __forceinline__ RawChunk<T> load_chunk(const T* p) {
+  RawChunk<T> r;
+  const uint4* s = reinterpret_cast<const uint4*>(p);
+  uint4* d = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(r) / 16; ++i) d[i] = s[i];
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store_chunk(T* p, const float (&f)[kChunk]) {
+  RawChunk<T> r;
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) r.v[i] = Elem<T>::from(f[i]);
+  const uint4* s = reinterpret_cast<const uint4*>(&r);
+  uint4* d = reinterpret_cast<uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(r) / 16; ++i) d[i] = s[i];
+}
+
+// ------------------------------------------------------- 8-bit checkpoints
+// A group of 32 neighbours shares the scale 2^e, e the smallest exponent
+// >= -126 for which its largest finite magnitude fits the code: at most 448
+// (E4M3) or below 127.5 (INT8, so that it rounds to at most 127). It is kept
+// as the byte e + 127, the exponent field of the fp32 number 2^e. A power of
+// two makes x 2^-e exact, so the code is the one rounding of the true value.
+// Values that are not finite become the NaN code (E4M3 0x7f, INT8 0x80).
+__device__ __forceinline__ uint32_t finite_abs_bits(float v) {
+  const uint32_t a = __float_as_uint(v) & 0x7FFFFFFFu;
+  return a < 0x7F800000u ? a : 0u;
+}
+
+__device__ __forceinline__ uint32_t ckpt_scale_byte(uint32_t amax_bits, int fmt) {
+  const int top = fmt == RAWINT4_CKPT_E4M3 ? 8 : 6;
+  const uint32_t limit = fmt == RAWINT4_CKPT_E4M3 ? 0x600000u : 0x7EFFFFu;  // mantissa bits of 1.75, just under 1.9921875
+  const int over = (amax_bits & 0x7FFFFFu) > limit ? 1 : 0;
+  return (uint32_t)max(1, (int)(amax_bits >> 23) - top + over);
+}
+
+// 2^-e of a scale byte written by ckpt_scale_byte (1 .. 249)
+__device__ __forceinline__ float ckpt_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+__device__ __forceinline__ float ckpt_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+__device__ __forceinline__ uint32_t ckpt_code(float x, float inv, int fmt) {
+  const bool finite = (__float_as_uint(x) & 0x7FFFFFFFu) < 0x7F800000u;
+  const float v = x * inv;
+  if (fmt == RAWINT4_CKPT_E4M3)
+    return finite ? (uint32_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3) : 0x7Fu;
+  return finite ? (uint32_t)__float2int_rn(v) & 0xFFu : 0x80u;
+}
+
+// Value of a code; |code| 2^e beyond fp32 gives an infinity.
+__device__ __forceinline__ float ckpt_value(uint32_t code, float scale, int fmt) {
+  if (fmt == RAWINT4_CKPT_E4M3) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
+    return __half2float(__half(h)) * scale;
+  }
+  const float v = (float)(int8_t)code * scale;
+  return code == 0x80u ? __uint_as_float(0x7FC00000u) : v;
+}
+
+// The group's largest value can round up past the type's largest number:
+// finite codes stay finite.
+__device__ __forceinline__ float ckpt_saturate(float v, float limit) {
+  return fabsf(v) > limit ? copysignf(limit, v) : v;
+}
+
+__device__ __forceinline__ float row_warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ------------------------------------------------------------- host side
+constexpr int64_t kMaxPitch = (int64_t)1 << 28;  // elements of a row pitch
+
+inline size_t type_size(int type) { return type == RAWINT4_TYPE_F32 ? 4 : 2; }
+inline bool type_ok(int type) {
+  return type == RAWINT4_TYPE_F32 || type == RAWINT4_TYPE_BF16 || type == RAWINT4_TYPE_F16;
+}
+inline bool ckpt_format_ok(int fmt) { return fmt == RAWINT4_CKPT_E4M3 || fmt == RAWINT4_CKPT_INT8; }
+inline int64_t ckpt_groups(int64_t width) { return (width + kCkptGroup - 1) / kCkptGroup; }
+
+// Every row of a [rows, width] tensor with row pitch ld starts on a 16-byte boundary.
+inline bool rows_aligned(const void* p, int64_t ld, int type) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)type_size(type) % 16 == 0;
+}
+// Bytes from the first to the last element of such a tensor.
+inline int64_t span_bytes(int64_t rows, int64_t width, int64_t ld, int64_t size) {
+  return rows > 0 ? ((rows - 1) * ld + width) * size : 0;
+}
+
+// A buffer of a call: its n bytes at p (null: absent) and the alignment of its elements.
+struct Span {
+  const void* p;
+  int64_t n;
+  int64_t align;
+};
+
+// Every buffer is aligned to its elements, and no output touches an input or another output.
+inline bool spans_ok(std::initializer_list<Span> in, std::initializer_list<Span> out) {
+  auto aligned = [](const Span& s) { return reinterpret_cast<uintptr_t>(s.p) % s.align == 0; };
+  auto apart = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return !a.p || !b.p || a.n <= 0 || b.n <= 0 || x >= y + (uintptr_t)b.n || y >= x + (uintptr_t)a.n;
+  };
+  for (const Span& s : in)
+    if (!aligned(s)) return false;
+  for (const Span* o = out.begin(); o != out.end(); ++o) {
+    if (!aligned(*o)) return false;
+    for (const Span& s : in)
+      if (!apart(*o, s)) return false;
+    for (const Span* q = out.begin(); q != o; ++q)
+      if (!apart(*o, *q)) return false;
+  }
+  return true;
+}
+
+}  // namespace r4
