@@ -12,137 +12,207 @@ namespace r4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // chunks a thread holds at once: 64 bytes of loads in flight
 
-// Vector layout: `cpr` chunks a row, padded to a multiple of four so that the
-// four lanes of a group never straddle rows.
-template <class T>
-__global__ void __launch_bounds__(kThreads) ckpt8_save_vec(const T* __restrict__ x, int64_t ldx, int64_t rows, int width,
-                                                           int cpr, int fmt, uint8_t* __restrict__ codes,
+// Where chunk i of a tensor lies. Chunks are counted over rows padded to
+// whole groups, so that the four lanes of a group never straddle rows; a
+// dense tensor of whole groups is one long row (cpr = 0) and needs no division.
+struct Place {
+  int64_t x, code, scale;  // element of x, code, scale byte
+  bool mine;
+};
+__device__ __forceinline__ Place place(int64_t i, uint32_t cpr, int width, int64_t ldx, int groups) {
+  if (cpr == 0) return {i * kChunk, i * kChunk, i / 4, true};
+  const uint32_t row = (uint32_t)i / cpr, c = (uint32_t)i - row * cpr;
+  return {row * ldx + c * kChunk, (int64_t)row * width + c * kChunk, (int64_t)row * groups + c / 4,
+          (int)(c * kChunk) < width};
+}
+
+// Vector layout.
+template <class T, int FMT>
+__global__ void __launch_bounds__(kThreads) ckpt8_save_vec(const T* __restrict__ x, int64_t ldx, int64_t n, int width,
+                                                           uint32_t cpr, uint8_t* __restrict__ codes,
                                                            uint8_t* __restrict__ scales, int groups) {
-  const int64_t n = rows * cpr;
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  // every lane of a warp runs the same number of turns: n is a multiple of four and
-  // the lanes past it take part in the shuffles with zeros
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads; i0 < n; i0 += stride) {
-    const int64_t i = i0 + threadIdx.x;
-    const int64_t row = i / cpr;
-    const int c = (int)(i - row * cpr);
-    const bool mine = i < n && c * kChunk < width;
-    float f[kChunk];
-    uint32_t amax = 0;
-    if (mine) {
-      const RawChunk<T> r = load_chunk(x + row * ldx + c * kChunk);
+  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  RawChunk<T> r[kUnroll];
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        f[j] = Elem<T>::to(r.v[j]);
-        amax = max(amax, finite_abs_bits(f[j]));
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u * kThreads;
+    r[u] = RawChunk<T>{};
+    if (i < n) {
+      const Place p = place(i, cpr, width, ldx, groups);
+      if (p.mine) r[u] = load_chunk(x + p.x);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u * kThreads;
+    float f[kChunk];
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) f[j] = Elem<T>::to(r[u].v[j]);
+    uint32_t byte;
+    const uint2 w = ckpt_encode8(f, FMT, &byte);
+    if (i < n) {
+      const Place p = place(i, cpr, width, ldx, groups);
+      if (p.mine) {
+        *reinterpret_cast<uint2*>(codes + p.code) = w;
+        if (threadIdx.x % 4 == 0) scales[p.scale] = (uint8_t)byte;
       }
     }
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    if (mine) {
-      const uint32_t byte = ckpt_scale_byte(amax, fmt);
-      const float inv = ckpt_inv_scale(byte);
-      uint32_t w[2] = {0u, 0u};
+  }
+}
+
+// Scalar layout: a warp takes kUnroll groups, n groups in all.
+template <class T>
+__global__ void __launch_bounds__(kThreads) ckpt8_save_any(const T* __restrict__ x, int64_t ldx, int64_t n, int width,
+                                                           int fmt, uint8_t* __restrict__ codes,
+                                                           uint8_t* __restrict__ scales, uint32_t groups) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
+  float f[kUnroll];
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) w[j / 4] |= ckpt_code(f[j], inv, fmt) << (8 * (j % 4));
-      *reinterpret_cast<uint2*>(codes + row * width + c * kChunk) = make_uint2(w[0], w[1]);
-      if (c % 4 == 0) scales[row * groups + c / 4] = (uint8_t)byte;
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t row = (uint32_t)(i0 + u) / groups;
+    const int col = (int)((uint32_t)(i0 + u) - row * groups) * kCkptGroup + lane;
+    f[u] = i0 + u < n && col < width ? Elem<T>::to(x[row * ldx + col]) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t row = (uint32_t)(i0 + u) / groups;
+    const int col = (int)((uint32_t)(i0 + u) - row * groups) * kCkptGroup + lane;
+    const uint32_t byte = ckpt_scale_byte(__reduce_max_sync(0xffffffffu, finite_abs_bits(f[u])), fmt);
+    if (i0 + u < n) {
+      if (col < width) codes[(int64_t)row * width + col] = (uint8_t)ckpt_code(f[u], ckpt_inv_scale(byte), fmt);
+      if (lane == 0) scales[i0 + u] = (uint8_t)byte;
     }
   }
 }
 
-// Scalar layout: one warp per group.
-template <class T>
-__global__ void __launch_bounds__(kThreads) ckpt8_save_any(const T* __restrict__ x, int64_t ldx, int64_t rows, int width,
-                                                           int fmt, uint8_t* __restrict__ codes,
-                                                           uint8_t* __restrict__ scales, int groups) {
-  const int lane = threadIdx.x & 31;
-  const int64_t n = rows * groups;
-  for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < n;
-       i += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int64_t row = i / groups;
-    const int g = (int)(i - row * groups);
-    const int col = g * kCkptGroup + lane;
-    const bool mine = col < width;
-    const float f = mine ? Elem<T>::to(x[row * ldx + col]) : 0.f;
-    const uint32_t byte = ckpt_scale_byte(__reduce_max_sync(0xffffffffu, finite_abs_bits(f)), fmt);
-    if (mine) codes[row * width + col] = (uint8_t)ckpt_code(f, ckpt_inv_scale(byte), fmt);
-    if (lane == 0) scales[i] = (uint8_t)byte;
-  }
-}
-
-template <class T>
+template <class T, int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt8_load_vec(const uint8_t* __restrict__ codes,
-                                                           const uint8_t* __restrict__ scales, int64_t rows, int width,
-                                                           int groups, int fmt, T* __restrict__ out) {
-  const int cpr = width / kChunk;
-  const int64_t n = rows * cpr;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / cpr;
-    const int c = (int)(i - row * cpr);
-    const uint2 w = *reinterpret_cast<const uint2*>(codes + i * kChunk);
-    const float scale = ckpt_scale(scales[row * groups + c / 4]);
-    float f[kChunk];
+                                                           const uint8_t* __restrict__ scales, int64_t n, int width,
+                                                           uint32_t cpr, int groups, T* __restrict__ out) {
+  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  uint2 w[kUnroll];
+  uint32_t byte[kUnroll];
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j)
-      f[j] = ckpt_saturate(ckpt_value(((j < 4 ? w.x : w.y) >> (8 * (j % 4))) & 0xFFu, scale, fmt), Elem<T>::kMax);
-    store_chunk(out + i * kChunk, f);
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u * kThreads;
+    w[u] = make_uint2(0u, 0u);
+    byte[u] = 1u;
+    if (i < n) {
+      const Place p = place(i, cpr, width, width, groups);
+      if (p.mine) {
+        w[u] = *reinterpret_cast<const uint2*>(codes + p.code);
+        byte[u] = scales[p.scale];
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u * kThreads;
+    float f[kChunk];
+    ckpt_decode8<T>(w[u], byte[u], FMT, f);
+    if (i < n) {
+      const Place p = place(i, cpr, width, width, groups);
+      if (p.mine) store_chunk(out + p.x, f);
+    }
   }
 }
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt8_load_any(const uint8_t* __restrict__ codes,
-                                                           const uint8_t* __restrict__ scales, int64_t rows, int width,
-                                                           int groups, int fmt, T* __restrict__ out) {
+                                                           const uint8_t* __restrict__ scales, int64_t n, int width,
+                                                           uint32_t groups, int fmt, T* __restrict__ out) {
   const int lane = threadIdx.x & 31;
-  const int64_t n = rows * groups;
-  for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < n;
-       i += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int64_t row = i / groups;
-    const int col = (int)(i - row * groups) * kCkptGroup + lane;
-    if (col < width) {
-      const float v = ckpt_value(codes[row * width + col], ckpt_scale(scales[i]), fmt);
-      out[row * width + col] = Elem<T>::from(ckpt_saturate(v, Elem<T>::kMax));
+  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
+  uint32_t code[kUnroll], byte[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t row = (uint32_t)(i0 + u) / groups;
+    const int col = (int)((uint32_t)(i0 + u) - row * groups) * kCkptGroup + lane;
+    const bool mine = i0 + u < n && col < width;
+    code[u] = mine ? codes[(int64_t)row * width + col] : 0u;
+    byte[u] = mine ? scales[i0 + u] : 1u;
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t row = (uint32_t)(i0 + u) / groups;
+    const int col = (int)((uint32_t)(i0 + u) - row * groups) * kCkptGroup + lane;
+    if (i0 + u < n && col < width) {
+      const float v = ckpt_value(code[u], ckpt_scale(byte[u]), fmt);
+      out[(int64_t)row * width + col] = Elem<T>::from(ckpt_saturate(v, Elem<T>::kMax));
     }
   }
 }
 
-int blocks_for(int64_t units, int per_block, int sms) {
-  const int64_t need = (units + per_block - 1) / per_block;
-  const int64_t most = (int64_t)sms * 16;
-  return (int)(need < most ? need : most);
+// Calls run(first row, units, blocks) for slices of at most 2^31 units (the
+// kernels' unit-to-row division is 32 bits wide), `per_row` units a row and
+// `per_block` a block.
+template <class F>
+cudaError_t slices(int64_t rows, int64_t per_row, int64_t per_block, F run) {
+  const int64_t step = ((int64_t)1 << 31) / per_row;
+  for (int64_t r = 0; r < rows; r += step) {
+    const int64_t n = (rows - r < step ? rows - r : step) * per_row;
+    run(r, n, (unsigned)((n + per_block - 1) / per_block));
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
 }
 
-template <class T>
-cudaError_t save(int fmt, int type, const void* x, int64_t ldx, int64_t rows, int width, uint8_t* codes, uint8_t* scales,
-                 int sms, cudaStream_t st) {
+constexpr int kGroupChunks = kCkptGroup / kChunk;
+constexpr int kVecUnits = kThreads * kUnroll;       // chunks of a block
+constexpr int kAnyUnits = kThreads / 32 * kUnroll;  // groups of a block
+
+uint32_t chunks_per_row(int width, int64_t ld) {
+  return ld == width && width % kCkptGroup == 0 ? 0u : (uint32_t)ckpt_groups(width) * kGroupChunks;
+}
+
+template <class T, int FMT>
+cudaError_t save(int type, const void* x, int64_t ldx, int64_t rows, int width, uint8_t* codes, uint8_t* scales,
+                 cudaStream_t st) {
   const int groups = (int)ckpt_groups(width);
   const T* p = static_cast<const T*>(x);
-  if (width % kChunk == 0 && rows_aligned(x, ldx, type) && reinterpret_cast<uintptr_t>(codes) % 8 == 0) {
-    const int cpr = groups * (kCkptGroup / kChunk);
-    ckpt8_save_vec<T><<<blocks_for(rows * cpr, kThreads, sms), kThreads, 0, st>>>(p, ldx, rows, width, cpr, fmt, codes,
-                                                                                  scales, groups);
-  } else {
-    ckpt8_save_any<T><<<blocks_for(rows * groups, kThreads / 32, sms), kThreads, 0, st>>>(p, ldx, rows, width, fmt, codes,
-                                                                                          scales, groups);
-  }
-  return cudaGetLastError();
+  if (width % kChunk == 0 && rows_aligned(x, ldx, type) && reinterpret_cast<uintptr_t>(codes) % 8 == 0)
+    return slices(rows, groups * kGroupChunks, kVecUnits, [&](int64_t r, int64_t n, unsigned blocks) {
+      ckpt8_save_vec<T, FMT><<<blocks, kThreads, 0, st>>>(p + r * ldx, ldx, n, width, chunks_per_row(width, ldx),
+                                                          codes + r * width, scales + r * groups, groups);
+    });
+  return slices(rows, groups, kAnyUnits, [&](int64_t r, int64_t n, unsigned blocks) {
+    ckpt8_save_any<T><<<blocks, kThreads, 0, st>>>(p + r * ldx, ldx, n, width, FMT, codes + r * width,
+                                                   scales + r * groups, groups);
+  });
+}
+
+template <class T, int FMT>
+cudaError_t load(int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int width, void* out,
+                 cudaStream_t st) {
+  const int groups = (int)ckpt_groups(width);
+  T* p = static_cast<T*>(out);
+  if (width % kChunk == 0 && rows_aligned(out, width, type) && reinterpret_cast<uintptr_t>(codes) % 8 == 0)
+    return slices(rows, groups * kGroupChunks, kVecUnits, [&](int64_t r, int64_t n, unsigned blocks) {
+      ckpt8_load_vec<T, FMT><<<blocks, kThreads, 0, st>>>(codes + r * width, scales + r * groups, n, width,
+                                                          chunks_per_row(width, width), groups, p + r * width);
+    });
+  return slices(rows, groups, kAnyUnits, [&](int64_t r, int64_t n, unsigned blocks) {
+    ckpt8_load_any<T><<<blocks, kThreads, 0, st>>>(codes + r * width, scales + r * groups, n, width, groups, FMT,
+                                                   p + r * width);
+  });
 }
 
 template <class T>
-cudaError_t load(int fmt, int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int width, void* out,
-                 int sms, cudaStream_t st) {
-  const int groups = (int)ckpt_groups(width);
-  T* p = static_cast<T*>(out);
-  if (width % kChunk == 0 && rows_aligned(out, width, type) && reinterpret_cast<uintptr_t>(codes) % 8 == 0) {
-    ckpt8_load_vec<T><<<blocks_for(rows * (width / kChunk), kThreads, sms), kThreads, 0, st>>>(codes, scales, rows, width,
-                                                                                               groups, fmt, p);
-  } else {
-    ckpt8_load_any<T><<<blocks_for(rows * groups, kThreads / 32, sms), kThreads, 0, st>>>(codes, scales, rows, width,
-                                                                                          groups, fmt, p);
-  }
-  return cudaGetLastError();
+cudaError_t save_fmt(int fmt, int type, const void* x, int64_t ldx, int64_t rows, int width, uint8_t* codes,
+                     uint8_t* scales, cudaStream_t st) {
+  return fmt == RAWINT4_CKPT_E4M3 ? save<T, RAWINT4_CKPT_E4M3>(type, x, ldx, rows, width, codes, scales, st)
+                                  : save<T, RAWINT4_CKPT_INT8>(type, x, ldx, rows, width, codes, scales, st);
+}
+
+template <class T>
+cudaError_t load_fmt(int fmt, int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int width, void* out,
+                     cudaStream_t st) {
+  return fmt == RAWINT4_CKPT_E4M3 ? load<T, RAWINT4_CKPT_E4M3>(type, codes, scales, rows, width, out, st)
+                                  : load<T, RAWINT4_CKPT_INT8>(type, codes, scales, rows, width, out, st);
 }
 
 bool sizes_ok(int fmt, int type, int64_t rows, int width, int64_t ld) {
@@ -172,9 +242,9 @@ RAWINT4_API int rawint4_ckpt8_save(int32_t format, int32_t type, const void* x, 
   cudaStream_t st = static_cast<cudaStream_t>(stream_);
   R4_PROF("ckpt8_save", st);
   cudaError_t err;
-  if (type == RAWINT4_TYPE_F32) err = save<float>(format, type, x, ldx, rows, width, codes, scales, sms, st);
-  else if (type == RAWINT4_TYPE_BF16) err = save<__nv_bfloat16>(format, type, x, ldx, rows, width, codes, scales, sms, st);
-  else err = save<__half>(format, type, x, ldx, rows, width, codes, scales, sms, st);
+  if (type == RAWINT4_TYPE_F32) err = save_fmt<float>(format, type, x, ldx, rows, width, codes, scales, st);
+  else if (type == RAWINT4_TYPE_BF16) err = save_fmt<__nv_bfloat16>(format, type, x, ldx, rows, width, codes, scales, st);
+  else err = save_fmt<__half>(format, type, x, ldx, rows, width, codes, scales, st);
   return err == cudaSuccess ? RAWINT4_OK : RAWINT4_CUDA_ERROR;
 }
 
@@ -192,9 +262,9 @@ RAWINT4_API int rawint4_ckpt8_load(int32_t format, const uint8_t* codes, const u
   cudaStream_t st = static_cast<cudaStream_t>(stream_);
   R4_PROF("ckpt8_load", st);
   cudaError_t err;
-  if (type == RAWINT4_TYPE_F32) err = load<float>(format, type, codes, scales, rows, width, out, sms, st);
-  else if (type == RAWINT4_TYPE_BF16) err = load<__nv_bfloat16>(format, type, codes, scales, rows, width, out, sms, st);
-  else err = load<__half>(format, type, codes, scales, rows, width, out, sms, st);
+  if (type == RAWINT4_TYPE_F32) err = load_fmt<float>(format, type, codes, scales, rows, width, out, st);
+  else if (type == RAWINT4_TYPE_BF16) err = load_fmt<__nv_bfloat16>(format, type, codes, scales, rows, width, out, st);
+  else err = load_fmt<__half>(format, type, codes, scales, rows, width, out, st);
   return err == cudaSuccess ? RAWINT4_OK : RAWINT4_CUDA_ERROR;
 }
 

@@ -7,12 +7,17 @@
 // x is a tensor, or the 8-bit checkpoint of one (rows.cuh), decoded on load;
 // the forward can write x's checkpoint in the same pass.
 //
-// A row lies in the registers of one warp (narrow rows, several warps a
-// block) or of one block, so each input is read once: the mean, then the
-// centred squares, are summed from registers in fp32. The backward keeps the
-// sums of dw and db over a block's rows in registers as well; each block
-// writes one partial row to the workspace and a second kernel adds the
-// partials in block order, so the result does not depend on timing.
+// Forward: a row lies in the registers of one warp (narrow rows, several rows
+// a block) or of one block, so the input is read once: the mean, then the
+// centred squares, are summed from registers in fp32.
+//
+// Backward: a fixed grid of blocks walks the rows. The threads of a row copy
+// their own chunks of the coming rows into shared memory (cp.async, a ring of
+// a few rows), so no barrier guards the ring and several rows are in flight
+// while one is computed. dw and db of a thread's columns stay in its
+// registers; each block writes one partial row of sums, and a second kernel,
+// launched early (its start overlaps the first one's tail), adds the partials
+// in block order, so the result does not depend on timing.
 #include "prof.cuh"
 #include "rows.cuh"
 
@@ -20,8 +25,11 @@ namespace r4 {
 namespace {
 
 constexpr int kMaxWidth = 16384;
-constexpr int kWarpRows = 4;        // rows a block works on at a time when a row lies in one warp
-constexpr int kMaxPartials = 296;   // blocks of the backward at most (two on each of 148 SMs): rows of partial sums
+constexpr int kFwdWarps = 8;         // rows of a forward block when a row lies in one warp
+constexpr int kBwdThreads = 512;     // threads of a backward block at most
+constexpr int kBwdBlocks = 148;      // blocks of the backward at most, one an SM: rows of partial sums
+constexpr int kBwdMaxStages = 4;     // rows in a thread group's ring
+constexpr int kBwdRing = 200 * 1024; // bytes of shared memory for the rings
 
 struct NormArgs {
   const void* x;            // elements of type T, or
@@ -45,343 +53,539 @@ struct NormArgs {
   void* gx;
   float* partial;           // [2][blocks][width]: dw, db
   int want_w, want_b;
+  int stages;
 };
 
-// Columns of this thread's element j of chunk i, in either layout.
+// Column of this thread's element j of chunk i, in either layout.
 template <bool VEC>
 __device__ __forceinline__ int column(int i, int j, int t, int threads) {
   return VEC ? (i * threads + t) * kChunk + j : (i * kChunk + j) * threads + t;
 }
 
+__device__ __forceinline__ float load_as(const void* p, int type, int64_t i) {
+  if (type == RAWINT4_TYPE_F32) return static_cast<const float*>(p)[i];
+  if (type == RAWINT4_TYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
 template <class T>
-__device__ __forceinline__ float any_load(const void* p, int64_t i) {
-  return Elem<T>::to(static_cast<const T*>(p)[i]);
-}
-__device__ __forceinline__ float vec_load(const void* p, int type, int i) {
-  if (type == RAWINT4_TYPE_F32) return any_load<float>(p, i);
-  if (type == RAWINT4_TYPE_BF16) return any_load<__nv_bfloat16>(p, i);
-  return any_load<__half>(p, i);
+__device__ __forceinline__ void widen(const RawChunk<T>& r, float (&v)[kChunk]) {
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) v[j] = Elem<T>::to(r.v[j]);
 }
 
-// Elements of one row of a tensor; columns past the width read as 0.
-template <class T, int NV, bool VEC>
-__device__ __forceinline__ void load_row(const T* row, int width, int t, int threads, float (&f)[NV * kChunk]) {
+__device__ __forceinline__ void fill(float (&v)[kChunk], float x) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (VEC) {
-      const int c0 = column<VEC>(i, 0, t, threads);
-      if (c0 < width) {
-        const RawChunk<T> r = load_chunk(row + c0);
+  for (int j = 0; j < kChunk; ++j) v[j] = x;
+}
+
+// The weight or bias of chunk i's columns; `none` where there is no tensor.
+template <bool VEC>
+__device__ __forceinline__ void load_vector(const void* p, int type, int i, int t, int threads, int width, float none,
+                                            float (&v)[kChunk]) {
+  if (!p) return fill(v, none);
+  if (VEC) {
+    const int c = column<true>(i, 0, t, threads);
+    if (c >= width) return fill(v, 0.f);
+    if (type == RAWINT4_TYPE_F32) widen(load_chunk(static_cast<const float*>(p) + c), v);
+    else if (type == RAWINT4_TYPE_BF16) widen(load_chunk(static_cast<const __nv_bfloat16*>(p) + c), v);
+    else widen(load_chunk(static_cast<const __half*>(p) + c), v);
+  } else {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) f[i * kChunk + j] = Elem<T>::to(r.v[j]);
-      } else {
+    for (int j = 0; j < kChunk; ++j) {
+      const int c = column<false>(i, j, t, threads);
+      v[j] = c < width ? load_as(p, type, c) : 0.f;
+    }
+  }
+}
+
+// Chunk i of a row in memory; columns past the width read as 0.
+template <class T, bool VEC>
+__device__ __forceinline__ RawChunk<T> row_chunk(const T* row, int i, int t, int threads, int width) {
+  RawChunk<T> r{};
+  if (VEC) {
+    const int c = column<true>(i, 0, t, threads);
+    if (c < width) r = load_chunk(row + c);
+  } else {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) f[i * kChunk + j] = 0.f;
-      }
-    } else {
+    for (int j = 0; j < kChunk; ++j) {
+      const int c = column<false>(i, j, t, threads);
+      if (c < width) r.v[j] = row[c];
+    }
+  }
+  return r;
+}
+
+// The same of a checkpointed row; values past fp32 saturate.
+template <bool VEC>
+__device__ __forceinline__ void ckpt_chunk(const uint8_t* codes, const uint8_t* scales, int fmt, int i, int t, int threads,
+                                           int width, float (&v)[kChunk]) {
+  fill(v, 0.f);
+  if (VEC) {
+    const int c = column<true>(i, 0, t, threads);
+    if (c < width) ckpt_decode8<float>(*reinterpret_cast<const uint2*>(codes + c), scales[c / kCkptGroup], fmt, v);
+  } else {
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int c = column<VEC>(i, j, t, threads);
-        f[i * kChunk + j] = c < width ? Elem<T>::to(row[c]) : 0.f;
+    for (int j = 0; j < kChunk; ++j) {
+      const int c = column<false>(i, j, t, threads);
+      if (c < width) v[j] = ckpt_saturate(ckpt_value(codes[c], ckpt_scale(scales[c / kCkptGroup]), fmt), FLT_MAX);
+    }
+  }
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ void store_row_chunk(T* row, int i, int t, int threads, int width, const float (&v)[kChunk]) {
+  if (VEC) {
+    const int c = column<true>(i, 0, t, threads);
+    if (c < width) store_chunk(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+      const int c = column<false>(i, j, t, threads);
+      if (c < width) row[c] = Elem<T>::from(v[j]);
+    }
+  }
+}
+
+// Writes the checkpoint of chunk i. Called by all lanes of a warp.
+template <bool VEC>
+__device__ __forceinline__ void save_chunk(const float (&v)[kChunk], uint8_t* codes, uint8_t* scales, int fmt, int i, int t,
+                                           int threads, int width) {
+  if (VEC) {
+    const int c = column<true>(i, 0, t, threads);
+    uint32_t byte;
+    const uint2 w = ckpt_encode8(v, fmt, &byte);
+    if (c < width) {
+      *reinterpret_cast<uint2*>(codes + c) = w;
+      if (c % kCkptGroup == 0) scales[c / kCkptGroup] = (uint8_t)byte;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+      const int c = column<false>(i, j, t, threads);
+      const uint32_t byte = ckpt_scale_byte(__reduce_max_sync(0xffffffffu, finite_abs_bits(v[j])), fmt);
+      if (c < width) {
+        codes[c] = (uint8_t)ckpt_code(v[j], ckpt_inv_scale(byte), fmt);
+        if (c % kCkptGroup == 0) scales[c / kCkptGroup] = (uint8_t)byte;
       }
     }
   }
 }
 
-template <class T, int NV, bool VEC>
-__device__ __forceinline__ void store_row(T* row, int width, int t, int threads, const float (&f)[NV * kChunk]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (VEC) {
-      const int c0 = column<VEC>(i, 0, t, threads);
-      if (c0 < width) {
-        float v[kChunk];
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] = f[i * kChunk + j];
-        store_chunk(row + c0, v);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int c = column<VEC>(i, j, t, threads);
-        if (c < width) row[c] = Elem<T>::from(f[i * kChunk + j]);
-      }
-    }
-  }
-}
-
-// The same from a checkpoint; values past fp32 saturate.
-template <int NV, bool VEC>
-__device__ __forceinline__ void load_ckpt_row(const uint8_t* codes, const uint8_t* scales, int fmt, int width, int t,
-                                              int threads, float (&f)[NV * kChunk]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (VEC) {
-      const int c0 = column<VEC>(i, 0, t, threads);
-      if (c0 < width) {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + c0);
-        const float s = ckpt_scale(scales[c0 / kCkptGroup]);
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j)
-          f[i * kChunk + j] = ckpt_saturate(ckpt_value(((j < 4 ? w.x : w.y) >> (8 * (j % 4))) & 0xFFu, s, fmt), FLT_MAX);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) f[i * kChunk + j] = 0.f;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int c = column<VEC>(i, j, t, threads);
-        f[i * kChunk + j] =
-            c < width ? ckpt_saturate(ckpt_value(codes[c], ckpt_scale(scales[c / kCkptGroup]), fmt), FLT_MAX) : 0.f;
-      }
-    }
-  }
-}
-
-// Sum over the threads of a row: a warp, or the block (through `buf`, which
-// the caller alternates so that one barrier a sum is enough).
-__device__ __forceinline__ float2 row_sum2(float a, float b, int threads, float2* buf) {
+// Sum over the `threads` threads of a row: one warp, or several that meet at
+// the named barrier `bar` (each sum has its own `buf`, or the callers alternate
+// between two).
+__device__ __forceinline__ float2 row_sum2(float a, float b, int threads, int bar, float2* buf) {
   a = row_warp_sum(a);
   b = row_warp_sum(b);
   if (threads == 32) return make_float2(a, b);
-  const int warps = threads >> 5;
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warps = threads >> 5;
+  if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
   const float2 v = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
   return make_float2(row_warp_sum(v.x), row_warp_sum(v.y));
 }
 
-// Writes the checkpoint of the row held in f. Called by all lanes of a warp.
-template <int NV, bool VEC>
-__device__ __forceinline__ void save_row(const float (&f)[NV * kChunk], uint8_t* codes, uint8_t* scales, int fmt,
-                                         int width, int t, int threads) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (VEC) {
-      const int c0 = column<VEC>(i, 0, t, threads);
-      uint32_t amax = 0;
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) amax = max(amax, finite_abs_bits(f[i * kChunk + j]));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      if (c0 < width) {
-        const uint32_t byte = ckpt_scale_byte(amax, fmt);
-        const float inv = ckpt_inv_scale(byte);
-        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) w[j / 4] |= ckpt_code(f[i * kChunk + j], inv, fmt) << (8 * (j % 4));
-        *reinterpret_cast<uint2*>(codes + c0) = make_uint2(w[0], w[1]);
-        if (c0 % kCkptGroup == 0) scales[c0 / kCkptGroup] = (uint8_t)byte;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int c = column<VEC>(i, j, t, threads);
-        const float v = f[i * kChunk + j];
-        const uint32_t byte = ckpt_scale_byte(__reduce_max_sync(0xffffffffu, finite_abs_bits(v)), fmt);
-        if (c < width) {
-          codes[c] = (uint8_t)ckpt_code(v, ckpt_inv_scale(byte), fmt);
-          if (c % kCkptGroup == 0) scales[c / kCkptGroup] = (uint8_t)byte;
-        }
-      }
-    }
-  }
-}
-
+// ------------------------------------------------------------------ forward
 // blockDim = (threads of a row, rows): the threads of a row are a warp when
-// blockDim.y > 1, else the block.
-template <class T, int NV, bool VEC, bool CKPT>
+// blockDim.y > 1, else the block. R is how a row waits in registers: as it
+// came (16-bit types in the vector layout), else as fp32.
+template <class T, class R, int NV, bool VEC, bool CKPT>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
   __shared__ float2 buf[2][16];
   const int t = threadIdx.x, threads = blockDim.x;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps leave; a block-wide row never does
-  float f[NV * kChunk];
-  if (CKPT)
-    load_ckpt_row<NV, VEC>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt, a.width,
-                           t, threads, f);
-  else
-    load_row<T, NV, VEC>(static_cast<const T*>(a.x) + row * a.ldx, a.width, t, threads, f);
-  if (!CKPT && a.codes)
-    save_row<NV, VEC>(f, a.codes + (int64_t)row * a.width, a.scales + (int64_t)row * a.groups, a.fmt, a.width, t, threads);
+  RawChunk<R> x[NV];
+  if constexpr (CKPT) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float v[kChunk];
+      ckpt_chunk<VEC>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt, i, t, threads,
+                      a.width, v);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) x[i].v[j] = v[j];
+    }
+  } else {
+    RawChunk<T> raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      raw[i] = row_chunk<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) x[i].v[j] = Elem<R>::from(Elem<T>::to(raw[i].v[j]));
+    if (a.codes)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float v[kChunk];
+        widen(x[i], v);
+        save_chunk<VEC>(v, a.codes + (int64_t)row * a.width, a.scales + (int64_t)row * a.groups, a.fmt, i, t, threads,
+                        a.width);
+      }
+  }
   const float inv_n = 1.0f / (float)a.width;
   float mu = 0.f;
   if (a.layer) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV * kChunk; ++i) s += f[i];
-    mu = row_sum2(s, 0.f, threads, buf[0]).x * inv_n;
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) s += Elem<R>::to(x[i].v[j]);
+    mu = row_sum2(s, 0.f, threads, 1, buf[0]).x * inv_n;
   }
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < kChunk; ++j) {
-      const float d = column<VEC>(i, j, t, threads) < a.width ? f[i * kChunk + j] - mu : 0.f;
-      f[i * kChunk + j] = d;
-      q += d * d;
+      const float d = Elem<R>::to(x[i].v[j]) - mu;
+      if (column<VEC>(i, VEC ? 0 : j, t, threads) < a.width) q += d * d;
     }
-  const float r = 1.0f / sqrtf(row_sum2(q, 0.f, threads, buf[1]).x * inv_n + a.eps);
+  const float r = 1.0f / sqrtf(row_sum2(q, 0.f, threads, 1, buf[1]).x * inv_n + a.eps);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    float w[kChunk], b[kChunk], v[kChunk];
+    load_vector<VEC>(a.weight, a.w_type, i, t, threads, a.width, 1.f, w);
+    load_vector<VEC>(a.bias, a.w_type, i, t, threads, a.width, 0.f, b);
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const int c = column<VEC>(i, j, t, threads);
-      if (c < a.width) {
-        float v = f[i * kChunk + j] * r;
-        if (a.weight) v *= vec_load(a.weight, a.w_type, c);
-        if (a.bias) v += vec_load(a.bias, a.w_type, c);
-        f[i * kChunk + j] = v;
-      }
-    }
-  store_row<T, NV, VEC>(static_cast<T*>(a.y) + (int64_t)row * a.width, a.width, t, threads, f);
+    for (int j = 0; j < kChunk; ++j) v[j] = (Elem<R>::to(x[i].v[j]) - mu) * r * w[j] + b[j];
+    store_row_chunk<T, VEC>(static_cast<T*>(a.y) + (int64_t)row * a.width, i, t, threads, a.width, v);
+  }
   if (t == 0) {
     if (a.mean) a.mean[row] = mu;
     a.rstd[row] = r;
   }
 }
 
-template <class T, int NV, bool VEC, bool CKPT>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
+// ----------------------------------------------------------------- backward
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Until at most n of this thread's groups are still on their way.
+__device__ __forceinline__ void copy_wait_but(int n) {
+  if (n >= 3) copy_wait<3>();
+  else if (n == 2) copy_wait<2>();
+  else if (n == 1) copy_wait<1>();
+  else copy_wait<0>();
+}
+
+// blockDim = (threads of a row, row groups); each group walks rows on its own
+// and meets at its own barrier. VEC: a thread's chunks of x and dy of a row lie
+// in its slots of the ring and are read from there twice, for the sums and for
+// dx; otherwise both reads go to memory (the second finds the row in cache).
+// The scale bytes of a checkpoint are fetched one row ahead into registers.
+template <class T, int NV, bool VEC, bool CKPT, bool SUMB>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a) {
   __shared__ float2 buf[2][16];
-  extern __shared__ float fold[];  // narrow rows: the warps' sums, [rows - 1][width] at a time
-  const int t = threadIdx.x, threads = blockDim.x;
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kXBytes = CKPT ? kChunk : (int)sizeof(RawChunk<T>);
+  const int t = threadIdx.x, threads = blockDim.x, group = threadIdx.y;
+  const int warp0 = group * (threads >> 5);  // a group's part of buf
+  const int step = gridDim.x * blockDim.y;
   const float inv_n = 1.0f / (float)a.width;
-  float dw[NV * kChunk], db[NV * kChunk], w[NV * kChunk];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // slots of this thread: [stage][chunk][thread], x behind dy
+  const int all = threads * blockDim.y, me = group * threads + t;
+  auto slot_g = [&](int stage, int i) { return ring + ((int64_t)(stage * NV + i) * all + me) * sizeof(RawChunk<T>); };
+  uint8_t* const ring_x = ring + (int64_t)a.stages * NV * all * sizeof(RawChunk<T>);
+  auto slot_x = [&](int stage, int i) { return ring_x + ((int64_t)(stage * NV + i) * all + me) * kXBytes; };
+  auto fetch = [&](int row, int stage) {
+    if (VEC && row < a.rows) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const int c = column<VEC>(i, j, t, threads);
-      dw[i * kChunk + j] = db[i * kChunk + j] = 0.f;
-      w[i * kChunk + j] = c < a.width ? (a.weight ? vec_load(a.weight, a.w_type, c) : 1.f) : 0.f;
+      for (int i = 0; i < NV; ++i) {
+        const int c = column<true>(i, 0, t, threads);
+        if (c < a.width) {
+          const T* g = static_cast<const T*>(a.gy) + row * a.ldg + c;
+          copy_async16(slot_g(stage, i), g);
+          if (sizeof(T) == 4) copy_async16(slot_g(stage, i) + 16, g + 4);
+          if (CKPT) {
+            copy_async8(slot_x(stage, i), a.in_codes + (int64_t)row * a.width + c);
+          } else {
+            const T* x = static_cast<const T*>(a.x) + row * a.ldx + c;
+            copy_async16(slot_x(stage, i), x);
+            if (sizeof(T) == 4) copy_async16(slot_x(stage, i) + 16, x + 4);
+          }
+        }
+      }
     }
-  int turn = 0;
-  for (int row = blockIdx.x * blockDim.y + threadIdx.y; row < a.rows; row += gridDim.x * blockDim.y, turn ^= 1) {
-    float f[NV * kChunk], g[NV * kChunk];
-    if (CKPT)
-      load_ckpt_row<NV, VEC>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt,
-                             a.width, t, threads, f);
-    else
-      load_row<T, NV, VEC>(static_cast<const T*>(a.x) + row * a.ldx, a.width, t, threads, f);
-    load_row<T, NV, VEC>(static_cast<const T*>(a.gy) + row * a.ldg, a.width, t, threads, g);
-    const float r = a.rstd_in[row], mu = a.layer ? a.mean_in[row] : 0.f;
+    if (VEC) copy_commit();
+  };
+
+  float dw[NV][kChunk], db[SUMB ? NV : 1][kChunk], w[NV][kChunk];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    fill(dw[i], 0.f);
+    if (SUMB) fill(db[i], 0.f);
+  }
+  const int first = blockIdx.x * blockDim.y + group;
+  for (int s = 0; s < a.stages; ++s) fetch(first + s * step, s);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) load_vector<VEC>(a.weight, a.w_type, i, t, threads, a.width, 1.f, w[i]);
+
+  uint32_t bytes[NV] = {};  // scale bytes of the row at hand
+  auto fetch_bytes = [&](int row, uint32_t (&b)[NV]) {
+    if (CKPT && VEC && row < a.rows)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = column<true>(i, 0, t, threads);
+        if (c < a.width) b[i] = a.in_scales[(int64_t)row * a.groups + c / kCkptGroup];
+      }
+  };
+  fetch_bytes(first, bytes);
+  float r = 0.f, mu = 0.f;
+  if (first < a.rows) {
+    r = a.rstd_in[first];
+    if (a.layer) mu = a.mean_in[first];
+  }
+
+  int stage = 0, turn = 0;
+  for (int row = first; row < a.rows; row += step) {
+    // x and dy of chunk i; columns past the width give 0 for dy and for w
+    auto chunk = [&](int i, float (&xv)[kChunk], float (&gv)[kChunk]) {
+      if (VEC) {
+        if (column<true>(i, 0, t, threads) < a.width) {
+          widen(*reinterpret_cast<const RawChunk<T>*>(slot_g(stage, i)), gv);
+          if (CKPT) ckpt_decode8<float>(*reinterpret_cast<const uint2*>(slot_x(stage, i)), bytes[i], a.in_fmt, xv);
+          else widen(*reinterpret_cast<const RawChunk<T>*>(slot_x(stage, i)), xv);
+        } else {
+          fill(gv, 0.f);
+          fill(xv, 0.f);
+        }
+      } else {
+        widen(row_chunk<T, false>(static_cast<const T*>(a.gy) + row * a.ldg, i, t, threads, a.width), gv);
+        if (CKPT)
+          ckpt_chunk<false>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt, i, t,
+                            threads, a.width, xv);
+        else
+          widen(row_chunk<T, false>(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width), xv);
+      }
+    };
+    const int next = row + step;
+    float next_r = 0.f, next_mu = 0.f;
+    uint32_t next_bytes[NV] = {};
+    if (next < a.rows) {
+      next_r = a.rstd_in[next];
+      if (a.layer) next_mu = a.mean_in[next];
+    }
+    fetch_bytes(next, next_bytes);
+    if (VEC) copy_wait_but(a.stages - 1);
+
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV * kChunk; ++i) {
-      const float xh = (f[i] - mu) * r, p = g[i] * w[i];
-      dw[i] += g[i] * xh;
-      db[i] += g[i];
-      f[i] = xh;
-      g[i] = p;
-      s1 += p;
-      s2 += p * xh;
+    for (int i = 0; i < NV; ++i) {
+      float xv[kChunk], gv[kChunk];
+      chunk(i, xv, gv);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const float xh = (xv[j] - mu) * r, p = gv[j] * w[i][j];
+        dw[i][j] += gv[j] * xh;
+        if (SUMB) db[i][j] += gv[j];
+        s1 += p;
+        s2 += p * xh;
+      }
     }
-    const float2 s = row_sum2(s1, s2, threads, buf[turn]);
+    const float2 s = row_sum2(s1, s2, threads, 1 + group, buf[turn] + warp0);
     const float m1 = a.layer ? s.x * inv_n : 0.f, m2 = s.y * inv_n;
 #pragma unroll
-    for (int i = 0; i < NV * kChunk; ++i) f[i] = r * (g[i] - m1 - f[i] * m2);
-    store_row<T, NV, VEC>(static_cast<T*>(a.gx) + (int64_t)row * a.width, a.width, t, threads, f);
+    for (int i = 0; i < NV; ++i) {
+      float xv[kChunk], gv[kChunk];
+      chunk(i, xv, gv);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) xv[j] = r * (gv[j] * w[i][j] - m1 - (xv[j] - mu) * r * m2);
+      store_row_chunk<T, VEC>(static_cast<T*>(a.gx) + (int64_t)row * a.width, i, t, threads, a.width, xv);
+    }
+    fetch(row + a.stages * step, stage);
+    stage = stage + 1 == a.stages ? 0 : stage + 1;
+    turn ^= 1;
+    r = next_r;
+    mu = next_mu;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) bytes[i] = next_bytes[i];
   }
+  if (VEC) copy_wait<0>();  // nothing but empty groups is left
   if (!a.want_w && !a.want_b) return;
+
+  // the block's groups, added in order in shared memory (the ring is free now)
+  float* fold = reinterpret_cast<float*>(ring);
+#pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     if (!(pass ? a.want_b : a.want_w)) continue;
-    if (blockDim.y > 1) {  // add the block's rows in order
+    float* out = a.partial + ((int64_t)pass * gridDim.x + blockIdx.x) * a.width;
+    for (int y = 0; y < (int)blockDim.y; ++y) {
       __syncthreads();
-      for (int y = 0; y < (int)blockDim.y; ++y) {
-        if ((int)threadIdx.y == y)
+      if (group == y)
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) {
-              const int c = column<VEC>(i, j, t, threads);
-              if (c < a.width) fold[c] = (y ? fold[c] : 0.f) + (pass ? db : dw)[i * kChunk + j];
+          for (int j = 0; j < kChunk; ++j) {
+            const int c = column<VEC>(i, j, t, threads);
+            if (c < a.width) {
+              const float v = (y ? fold[c] : 0.f) + (pass ? db[SUMB ? i : 0][j] : dw[i][j]);
+              if (y + 1 == (int)blockDim.y) out[c] = v;
+              else fold[c] = v;
             }
-        __syncthreads();
-      }
-      float* out = a.partial + ((int64_t)pass * gridDim.x + blockIdx.x) * a.width;
-      for (int c = threadIdx.y * threads + t; c < a.width; c += threads * blockDim.y) out[c] = fold[c];
-    } else {
-      float* out = a.partial + ((int64_t)pass * gridDim.x + blockIdx.x) * a.width;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          const int c = column<VEC>(i, j, t, threads);
-          if (c < a.width) out[c] = (pass ? db : dw)[i * kChunk + j];
-        }
+          }
     }
   }
 }
 
-// out = (accumulate ? out : 0) + the partial rows in order, rounded once.
-__global__ void __launch_bounds__(256) norm_fold_kernel(const float* __restrict__ partial, int blocks, int width,
-                                                        void* gw, void* gb, int type, int accumulate) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+// out = (accumulate ? out : 0) + the sum of the partial rows, rounded once.
+// A warp reads 32 neighbouring columns of every 16th row; the 16 sums are
+// added in order.
+constexpr int kFoldWarps = 16;
+__global__ void __launch_bounds__(32 * kFoldWarps) norm_fold_kernel(const float* __restrict__ partial, int blocks,
+                                                                    int width, void* gw, void* gb, int type,
+                                                                    int accumulate) {
+  __shared__ float sums[kFoldWarps][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial rows are complete and visible
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   void* out = blockIdx.y ? gb : gw;
-  if (c >= width || !out) return;
+  if (!out) return;
   const float* p = partial + (int64_t)blockIdx.y * blocks * width + c;
-  float s = accumulate ? vec_load(out, type, c) : 0.f;
-  for (int b = 0; b < blocks; ++b) s += p[(int64_t)b * width];
+  float s = 0.f;
+  if (c < width)
+#pragma unroll 4
+    for (int b = warp; b < blocks; b += kFoldWarps) s += p[(int64_t)b * width];
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || c >= width) return;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kFoldWarps; ++i) s += sums[i][lane];
+  if (accumulate) s += load_as(out, type, c);
   if (type == RAWINT4_TYPE_F32) static_cast<float*>(out)[c] = s;
   else if (type == RAWINT4_TYPE_BF16) static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(s);
   else static_cast<__half*>(out)[c] = __float2half_rn(s);
 }
 
+// ------------------------------------------------------------- launch shapes
 struct Shape {
-  int nv, threads, rows;  // chunks a thread, threads a row, rows a block
+  int nv, threads, rows;  // chunks a thread, threads a row, rows (row groups) a block
 };
 
-Shape shape_for(int width) {
-  const int chunks = (width + kChunk - 1) / kChunk;
-  if (chunks <= 32) return {1, 32, kWarpRows};
-  if (chunks <= 64) return {2, 32, kWarpRows};
-  if (chunks <= 128) return {4, 32, kWarpRows};
-  const int nv = chunks <= 512 ? 2 : 4;
-  return {nv, (chunks + nv * 32 - 1) / (nv * 32) * 32, 1};
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The smallest of `most`, most / 2, ... chunks a thread that a row of one warp
+// needs, else `most` and as many warps as that takes.
+Shape shape_for(int width, int most, int warps_rows) {
+  const int chunks = ceil_div(width, kChunk);
+  for (int nv = 1; nv <= most && nv <= 4; nv *= 2)
+    if (chunks <= 32 * nv) return {nv, 32, warps_rows};
+  return {most, ceil_div(chunks, most * 32) * 32, 1};
+}
+
+// Forward: 16-bit rows wait in registers as they came, so a thread can hold eight chunks.
+Shape fwd_shape(const NormArgs& a, int type, bool vec) {
+  return shape_for(a.width, vec && !a.in_codes && type != RAWINT4_TYPE_F32 ? 8 : 4, kFwdWarps);
+}
+
+Shape bwd_shape(int width) {
+  Shape s = shape_for(width, 4, 1);
+  s.rows = kBwdThreads / s.threads;
+  return s;
 }
 
 int bwd_blocks(const Shape& s, int rows) {
-  const int need = (rows + s.rows - 1) / s.rows;
-  return need < kMaxPartials ? need : kMaxPartials;
+  const int need = ceil_div(rows, s.rows);
+  return need < kBwdBlocks ? need : kBwdBlocks;
 }
 
-template <class T, int NV, bool VEC, bool CKPT>
-cudaError_t launch(const NormArgs& a, const Shape& s, bool bwd, cudaStream_t st) {
-  const dim3 block(s.threads, s.rows);
-  if (bwd)
-    norm_bwd_kernel<T, NV, VEC, CKPT>
-        <<<bwd_blocks(s, a.rows), block, s.rows > 1 ? a.width * sizeof(float) : 0, st>>>(a);
-  else
-    norm_fwd_kernel<T, NV, VEC, CKPT><<<(a.rows + s.rows - 1) / s.rows, block, 0, st>>>(a);
+// Bytes of one stage of a block's rings.
+int stage_bytes(const Shape& s, int type, bool ckpt) {
+  const int chunk = kChunk * (int)type_size(type);
+  return s.nv * s.threads * s.rows * (chunk + (ckpt ? kChunk : chunk));
+}
+
+template <class T, int NV, bool VEC, bool CKPT, bool SUMB>
+cudaError_t launch_bwd(NormArgs a, int type, cudaStream_t st) {
+  const Shape s = bwd_shape(a.width);
+  const int stage = stage_bytes(s, type, CKPT);
+  a.stages = VEC ? kBwdRing / stage : 1;
+  if (a.stages > kBwdMaxStages) a.stages = kBwdMaxStages;
+  int smem = VEC ? a.stages * stage : 0;
+  if (smem < a.width * (int)sizeof(float)) smem = a.width * (int)sizeof(float);
+  static std::atomic<unsigned long long> opted{0};
+  int dev = 0;
+  if (!device_flag_test(opted, &dev)) {
+    const cudaError_t err = cudaFuncSetAttribute(norm_bwd_kernel<T, NV, VEC, CKPT, SUMB>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdRing);
+    if (err != cudaSuccess) return err;
+    device_flag_set(opted, dev);
+  }
+  norm_bwd_kernel<T, NV, VEC, CKPT, SUMB><<<bwd_blocks(s, a.rows), dim3(s.threads, s.rows), smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <class T, class R, int NV, bool VEC, bool CKPT>
+cudaError_t launch_fwd(const NormArgs& a, const Shape& s, cudaStream_t st) {
+  norm_fwd_kernel<T, R, NV, VEC, CKPT><<<ceil_div(a.rows, s.rows), dim3(s.threads, s.rows), 0, st>>>(a);
   return cudaGetLastError();
 }
 
 template <class T, int NV>
-cudaError_t pick(const NormArgs& a, const Shape& s, bool vec, bool bwd, cudaStream_t st) {
+cudaError_t pick_fwd(const NormArgs& a, const Shape& s, bool vec, cudaStream_t st) {
   if (a.in_codes)
-    return vec ? launch<T, NV, true, true>(a, s, bwd, st) : launch<T, NV, false, true>(a, s, bwd, st);
-  return vec ? launch<T, NV, true, false>(a, s, bwd, st) : launch<T, NV, false, false>(a, s, bwd, st);
+    return vec ? launch_fwd<T, float, NV, true, true>(a, s, st) : launch_fwd<T, float, NV, false, true>(a, s, st);
+  return vec ? launch_fwd<T, T, NV, true, false>(a, s, st) : launch_fwd<T, float, NV, false, false>(a, s, st);
 }
 
 template <class T>
-cudaError_t pick_nv(const NormArgs& a, const Shape& s, bool vec, bool bwd, cudaStream_t st) {
-  if (s.nv == 1) return pick<T, 1>(a, s, vec, bwd, st);
-  if (s.nv == 2) return pick<T, 2>(a, s, vec, bwd, st);
-  return pick<T, 4>(a, s, vec, bwd, st);
+cudaError_t run_fwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
+  const Shape s = fwd_shape(a, type, vec);
+  if constexpr (sizeof(T) == 2)
+    if (s.nv == 8) return launch_fwd<T, T, 8, true, false>(a, s, st);
+  if (s.nv == 1) return pick_fwd<T, 1>(a, s, vec, st);
+  if (s.nv == 2) return pick_fwd<T, 2>(a, s, vec, st);
+  return pick_fwd<T, 4>(a, s, vec, st);
 }
 
-cudaError_t run(const NormArgs& a, int type, bool vec, bool bwd, cudaStream_t st) {
-  const Shape s = shape_for(a.width);
-  if (type == RAWINT4_TYPE_F32) return pick_nv<float>(a, s, vec, bwd, st);
-  if (type == RAWINT4_TYPE_BF16) return pick_nv<__nv_bfloat16>(a, s, vec, bwd, st);
-  return pick_nv<__half>(a, s, vec, bwd, st);
+template <class T, int NV, bool VEC, bool CKPT>
+cudaError_t pick_sums(const NormArgs& a, int type, cudaStream_t st) {
+  return a.want_b ? launch_bwd<T, NV, VEC, CKPT, true>(a, type, st) : launch_bwd<T, NV, VEC, CKPT, false>(a, type, st);
+}
+
+template <class T, int NV>
+cudaError_t pick_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
+  if (a.in_codes) return vec ? pick_sums<T, NV, true, true>(a, type, st) : pick_sums<T, NV, false, true>(a, type, st);
+  return vec ? pick_sums<T, NV, true, false>(a, type, st) : pick_sums<T, NV, false, false>(a, type, st);
+}
+
+template <class T>
+cudaError_t run_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
+  const int nv = bwd_shape(a.width).nv;
+  if (nv == 1) return pick_bwd<T, 1>(a, type, vec, st);
+  if (nv == 2) return pick_bwd<T, 2>(a, type, vec, st);
+  return pick_bwd<T, 4>(a, type, vec, st);
+}
+
+// The second kernel may start while the first one ends; it waits for it itself.
+cudaError_t launch_fold(const float* partial, int blocks, int width, void* gw, void* gb, int type, int accumulate,
+                        cudaStream_t st) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ceil_div(width, 32), 2);
+  cfg.blockDim = dim3(32 * kFoldWarps);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_fold_kernel, partial, blocks, width, gw, gb, type, accumulate);
 }
 
 bool cfg_ok(const rawint4_norm_cfg* c) {
-  return c && c->rows >= 0 && c->width >= 1 && c->width <= kMaxWidth && type_ok(c->type) && type_ok(c->weight_type) &&
+  return c && c->rows >= 0 && c->rows <= 1 << 30 && c->width >= 1 && c->width <= kMaxWidth && type_ok(c->type) && type_ok(c->weight_type) &&
          (c->kind == RAWINT4_NORM_LAYER || c->kind == RAWINT4_NORM_RMS) && c->eps > 0.f && c->eps <= FLT_MAX;
 }
 
@@ -404,6 +608,8 @@ bool input_aligned(const NormArgs& a, int type) {
   return a.width % kChunk == 0 &&
          (a.in_codes ? reinterpret_cast<uintptr_t>(a.in_codes) % 8 == 0 : rows_aligned(a.x, a.ldx, type));
 }
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 NormArgs common_args(const rawint4_norm_cfg* c, const void* weight) {
   NormArgs a{};
@@ -452,16 +658,20 @@ RAWINT4_API int rawint4_norm_fwd(const rawint4_norm_cfg* cfg, const void* x, int
   a.codes = save_codes;
   a.scales = save_scales;
   a.fmt = save_format;
-  const bool vec = input_aligned(a, cfg->type) && rows_aligned(y, a.width, cfg->type) &&
-                   reinterpret_cast<uintptr_t>(save_codes) % 8 == 0;
+  const bool vec = input_aligned(a, cfg->type) && rows_aligned(y, a.width, cfg->type) && aligned16(weight) &&
+                   aligned16(bias) && reinterpret_cast<uintptr_t>(save_codes) % 8 == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream_);
   R4_PROF("norm_fwd", st);
-  return run(a, cfg->type, vec, false, st) == cudaSuccess ? RAWINT4_OK : RAWINT4_CUDA_ERROR;
+  cudaError_t err;
+  if (cfg->type == RAWINT4_TYPE_F32) err = run_fwd<float>(a, cfg->type, vec, st);
+  else if (cfg->type == RAWINT4_TYPE_BF16) err = run_fwd<__nv_bfloat16>(a, cfg->type, vec, st);
+  else err = run_fwd<__half>(a, cfg->type, vec, st);
+  return err == cudaSuccess ? RAWINT4_OK : RAWINT4_CUDA_ERROR;
 }
 
 RAWINT4_API int rawint4_norm_bwd_workspace_size(const rawint4_norm_cfg* cfg, size_t* bytes) {
   if (!cfg_ok(cfg) || !bytes) return RAWINT4_INVALID_ARGUMENT;
-  const size_t n = (size_t)2 * bwd_blocks(shape_for(cfg->width), cfg->rows) * cfg->width * sizeof(float);
+  const size_t n = (size_t)2 * bwd_blocks(bwd_shape(cfg->width), cfg->rows) * cfg->width * sizeof(float);
   *bytes = (n + 255) / 256 * 256;
   return RAWINT4_OK;
 }
@@ -500,15 +710,19 @@ RAWINT4_API int rawint4_norm_bwd(const rawint4_norm_cfg* cfg, const void* x, int
   cudaStream_t st = static_cast<cudaStream_t>(stream_);
   if (a.rows > 0) {
     const bool vec = input_aligned(a, cfg->type) && rows_aligned(grad_y, ldg, cfg->type) &&
-                     rows_aligned(grad_x, a.width, cfg->type);
+                     rows_aligned(grad_x, a.width, cfg->type) && aligned16(weight);
     R4_PROF("norm_bwd", st);
-    if (run(a, cfg->type, vec, true, st) != cudaSuccess) return RAWINT4_CUDA_ERROR;
+    cudaError_t err;
+    if (cfg->type == RAWINT4_TYPE_F32) err = run_bwd<float>(a, cfg->type, vec, st);
+    else if (cfg->type == RAWINT4_TYPE_BF16) err = run_bwd<__nv_bfloat16>(a, cfg->type, vec, st);
+    else err = run_bwd<__half>(a, cfg->type, vec, st);
+    if (err != cudaSuccess) return RAWINT4_CUDA_ERROR;
   }
   if (sums) {
     R4_PROF("norm_fold", st);
-    norm_fold_kernel<<<dim3((a.width + 255) / 256, 2), 256, 0, st>>>(
-        a.partial, bwd_blocks(shape_for(a.width), a.rows), a.width, grad_weight, grad_bias, cfg->weight_type, accumulate);
-    if (cudaGetLastError() != cudaSuccess) return RAWINT4_CUDA_ERROR;
+    if (launch_fold(a.partial, bwd_blocks(bwd_shape(a.width), a.rows), a.width, grad_weight, grad_bias, cfg->weight_type,
+                    accumulate, st) != cudaSuccess)
+      return RAWINT4_CUDA_ERROR;
   }
   return RAWINT4_OK;
 }

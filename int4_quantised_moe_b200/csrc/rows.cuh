@@ -92,12 +92,70 @@ __device__ __forceinline__ uint32_t ckpt_scale_byte(uint32_t amax_bits, int fmt)
 __device__ __forceinline__ float ckpt_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 __device__ __forceinline__ float ckpt_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+__device__ __forceinline__ bool is_finite_bits(uint32_t abs_bits) { return abs_bits < 0x7F800000u; }
+
 __device__ __forceinline__ uint32_t ckpt_code(float x, float inv, int fmt) {
-  const bool finite = (__float_as_uint(x) & 0x7FFFFFFFu) < 0x7F800000u;
+  const bool finite = is_finite_bits(__float_as_uint(x) & 0x7FFFFFFFu);
   const float v = x * inv;
   if (fmt == RAWINT4_CKPT_E4M3)
     return finite ? (uint32_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3) : 0x7Fu;
   return finite ? (uint32_t)__float2int_rn(v) & 0xFFu : 0x80u;
+}
+
+// Eight codes of finite values (INT8: adding 1.5 2^23 leaves the rounded
+// integer in the low mantissa bits).
+__device__ __forceinline__ uint2 ckpt_codes8(const float (&f)[kChunk], float inv, int fmt) {
+  uint32_t w[2];
+  if (fmt == RAWINT4_CKPT_E4M3) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h] * inv, f[4 * h + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi =
+          __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h + 2] * inv, f[4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+      w[h] = lo | hi << 16;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(fmaf(f[4 * h + j], inv, 12582912.f));  // exact product, one rounding
+      w[h] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// The chunk's share of a group's largest magnitude: bits of |x|, infinities
+// and NaN included.
+__device__ __forceinline__ uint32_t abs_bits8(const float (&f)[kChunk]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// Codes and scale byte of a chunk whose group lies in four neighbouring
+// lanes; called by all lanes of a warp (a lane without a chunk passes zeros).
+__device__ __forceinline__ uint2 ckpt_encode8(const float (&f)[kChunk], int fmt, uint32_t* byte) {
+  uint32_t amax = abs_bits8(f);
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  if (__any_sync(0xffffffffu, !is_finite_bits(amax))) {  // rare: leave such values out of the scale, code them as NaN
+    amax = 0;
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) amax = max(amax, finite_abs_bits(f[j]));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    *byte = ckpt_scale_byte(amax, fmt);
+    const float inv = ckpt_inv_scale(*byte);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) w[j / 4] |= ckpt_code(f[j], inv, fmt) << (8 * (j % 4));
+    return make_uint2(w[0], w[1]);
+  }
+  *byte = ckpt_scale_byte(amax, fmt);
+  return ckpt_codes8(f, ckpt_inv_scale(*byte), fmt);
 }
 
 // Value of a code; |code| 2^e beyond fp32 gives an infinity.
@@ -114,6 +172,43 @@ __device__ __forceinline__ float ckpt_value(uint32_t code, float scale, int fmt)
 // finite codes stay finite.
 __device__ __forceinline__ float ckpt_saturate(float v, float limit) {
   return fabsf(v) > limit ? copysignf(limit, v) : v;
+}
+
+// The largest scale byte under which every finite code stays below `limit`:
+// 448 2^e and 127 2^e fit fp16 up to e = 7 and 9, fp32 and bf16 up to 119 and 121.
+template <class T>
+__device__ __forceinline__ uint32_t ckpt_safe_byte(int fmt) {
+  return (sizeof(T) == 2 && Elem<T>::kMax < 1e5f ? 127u + 7u : 127u + 119u) + (fmt == RAWINT4_CKPT_E4M3 ? 0u : 2u);
+}
+
+// Eight values of a checkpoint, saturated for type T.
+template <class T>
+__device__ __forceinline__ void ckpt_decode8(uint2 w, uint32_t byte, int fmt, float (&f)[kChunk]) {
+  const float scale = ckpt_scale(byte);
+  if (fmt == RAWINT4_CKPT_E4M3) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t two = ((q < 2 ? w.x : w.y) >> (16 * (q & 1))) & 0xFFFFu;
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+      const float2 v = __half22float2(__half2(h));
+      f[2 * q] = v.x * scale;
+      f[2 * q + 1] = v.y * scale;
+    }
+  } else {
+    const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};  // code + 128 in the low bits of 2^23
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j)
+      f[j] = (__uint_as_float(__byte_perm(u[j / 4], 0x4B000000u, 0x7440 + j % 4)) - 8388736.f) * scale;
+    if (__vcmpeq4(w.x, 0x80808080u) | __vcmpeq4(w.y, 0x80808080u)) {
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j)
+        if ((u[j / 4] >> (8 * (j % 4)) & 0xFFu) == 0u) f[j] = __uint_as_float(0x7FC00000u);
+    }
+  }
+  if (byte > ckpt_safe_byte<T>(fmt)) {
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) f[j] = ckpt_saturate(f[j], Elem<T>::kMax);
+  }
 }
 
 __device__ __forceinline__ float row_warp_sum(float v) {
