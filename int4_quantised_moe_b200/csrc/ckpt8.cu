@@ -47,11 +47,8 @@ __global__ void __launch_bounds__(kThreads) ckpt8_save_vec(const T* __restrict__
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t i = i0 + u * kThreads;
-    float f[kChunk];
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) f[j] = Elem<T>::to(r[u].v[j]);
     uint32_t byte;
-    const uint2 w = ckpt_encode8(f, FMT, &byte);
+    const uint2 w = ckpt_encode8(widen<T>(r[u]), abs_max_bits<T>(r[u]), FMT, &byte);
     if (i < n) {
       const Place p = place(i, cpr, width, ldx, groups);
       if (p.mine) {
@@ -111,8 +108,7 @@ __global__ void __launch_bounds__(kThreads) ckpt8_load_vec(const uint8_t* __rest
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t i = i0 + u * kThreads;
-    float f[kChunk];
-    ckpt_decode8<T>(w[u], byte[u], FMT, f);
+    const Chunk f = ckpt_decode8<T>(w[u], byte[u], FMT);
     if (i < n) {
       const Place p = place(i, cpr, width, width, groups);
       if (p.mine) store_chunk(out + p.x, f);

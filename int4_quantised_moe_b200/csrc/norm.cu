@@ -68,73 +68,58 @@ __device__ __forceinline__ float load_as(const void* p, int type, int64_t i) {
   return __half2float(static_cast<const __half*>(p)[i]);
 }
 
-template <class T>
-__device__ __forceinline__ void widen(const RawChunk<T>& r, float (&v)[kChunk]) {
-#pragma unroll
-  for (int j = 0; j < kChunk; ++j) v[j] = Elem<T>::to(r.v[j]);
-}
-
-__device__ __forceinline__ void fill(float (&v)[kChunk], float x) {
-#pragma unroll
-  for (int j = 0; j < kChunk; ++j) v[j] = x;
-}
-
 // The weight or bias of chunk i's columns; `none` where there is no tensor.
 template <bool VEC>
-__device__ __forceinline__ void load_vector(const void* p, int type, int i, int t, int threads, int width, float none,
-                                            float (&v)[kChunk]) {
-  if (!p) return fill(v, none);
+__device__ __forceinline__ Chunk load_vector(const void* p, int type, int i, int t, int threads, int width, float none) {
+  if (!p) return chunk_of(none);
   if (VEC) {
     const int c = column<true>(i, 0, t, threads);
-    if (c >= width) return fill(v, 0.f);
-    if (type == RAWINT4_TYPE_F32) widen(load_chunk(static_cast<const float*>(p) + c), v);
-    else if (type == RAWINT4_TYPE_BF16) widen(load_chunk(static_cast<const __nv_bfloat16*>(p) + c), v);
-    else widen(load_chunk(static_cast<const __half*>(p) + c), v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const int c = column<false>(i, j, t, threads);
-      v[j] = c < width ? load_as(p, type, c) : 0.f;
-    }
+    if (c >= width) return chunk_of(0.f);
+    if (type == RAWINT4_TYPE_F32) return widen<float>(load_chunk(static_cast<const float*>(p) + c));
+    if (type == RAWINT4_TYPE_BF16) return widen<__nv_bfloat16>(load_chunk(static_cast<const __nv_bfloat16*>(p) + c));
+    return widen<__half>(load_chunk(static_cast<const __half*>(p) + c));
   }
+  Chunk v;
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) {
+    const int c = column<false>(i, j, t, threads);
+    v[j] = c < width ? load_as(p, type, c) : 0.f;
+  }
+  return v;
 }
 
-// Chunk i of a row in memory; columns past the width read as 0.
-template <class T, bool VEC>
-__device__ __forceinline__ RawChunk<T> row_chunk(const T* row, int i, int t, int threads, int width) {
-  RawChunk<T> r{};
-  if (VEC) {
-    const int c = column<true>(i, 0, t, threads);
-    if (c < width) r = load_chunk(row + c);
-  } else {
+// Chunk i of a row in memory, in the scalar layout; columns past the width read as 0.
+template <class T>
+__device__ __forceinline__ Chunk any_chunk(const T* row, int i, int t, int threads, int width) {
+  Chunk v;
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const int c = column<false>(i, j, t, threads);
-      if (c < width) r.v[j] = row[c];
-    }
+  for (int j = 0; j < kChunk; ++j) {
+    const int c = column<false>(i, j, t, threads);
+    v[j] = c < width ? Elem<T>::to(row[c]) : 0.f;
   }
-  return r;
+  return v;
 }
 
-// The same of a checkpointed row; values past fp32 saturate.
+// Chunk i of a checkpointed row; values past fp32 saturate.
 template <bool VEC>
-__device__ __forceinline__ void ckpt_chunk(const uint8_t* codes, const uint8_t* scales, int fmt, int i, int t, int threads,
-                                           int width, float (&v)[kChunk]) {
-  fill(v, 0.f);
+__device__ __forceinline__ Chunk ckpt_chunk(const uint8_t* codes, const uint8_t* scales, int fmt, int i, int t, int threads,
+                                            int width) {
   if (VEC) {
     const int c = column<true>(i, 0, t, threads);
-    if (c < width) ckpt_decode8<float>(*reinterpret_cast<const uint2*>(codes + c), scales[c / kCkptGroup], fmt, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const int c = column<false>(i, j, t, threads);
-      if (c < width) v[j] = ckpt_saturate(ckpt_value(codes[c], ckpt_scale(scales[c / kCkptGroup]), fmt), FLT_MAX);
-    }
+    return c < width ? ckpt_decode8<float>(*reinterpret_cast<const uint2*>(codes + c), scales[c / kCkptGroup], fmt)
+                     : chunk_of(0.f);
   }
+  Chunk v;
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) {
+    const int c = column<false>(i, j, t, threads);
+    v[j] = c < width ? ckpt_saturate(ckpt_value(codes[c], ckpt_scale(scales[c / kCkptGroup]), fmt), FLT_MAX) : 0.f;
+  }
+  return v;
 }
 
 template <class T, bool VEC>
-__device__ __forceinline__ void store_row_chunk(T* row, int i, int t, int threads, int width, const float (&v)[kChunk]) {
+__device__ __forceinline__ void store_row_chunk(T* row, int i, int t, int threads, int width, const Chunk& v) {
   if (VEC) {
     const int c = column<true>(i, 0, t, threads);
     if (c < width) store_chunk(row + c, v);
@@ -148,13 +133,14 @@ __device__ __forceinline__ void store_row_chunk(T* row, int i, int t, int thread
 }
 
 // Writes the checkpoint of chunk i. Called by all lanes of a warp.
-template <bool VEC>
-__device__ __forceinline__ void save_chunk(const float (&v)[kChunk], uint8_t* codes, uint8_t* scales, int fmt, int i, int t,
+template <class R, bool VEC>
+__device__ __forceinline__ void save_chunk(const RawChunk<R>& raw, uint8_t* codes, uint8_t* scales, int fmt, int i, int t,
                                            int threads, int width) {
+  const Chunk v = widen<R>(raw);
   if (VEC) {
     const int c = column<true>(i, 0, t, threads);
     uint32_t byte;
-    const uint2 w = ckpt_encode8(v, fmt, &byte);
+    const uint2 w = ckpt_encode8(v, abs_max_bits<R>(raw), fmt, &byte);
     if (c < width) {
       *reinterpret_cast<uint2*>(codes + c) = w;
       if (c % kCkptGroup == 0) scales[c / kCkptGroup] = (uint8_t)byte;
@@ -191,65 +177,78 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int threads, int ba
 // blockDim.y > 1, else the block. R is how a row waits in registers: as it
 // came (16-bit types in the vector layout), else as fp32.
 template <class T, class R, int NV, bool VEC, bool CKPT>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(512, 2) norm_fwd_kernel(const NormArgs a) {
   __shared__ float2 buf[2][16];
   const int t = threadIdx.x, threads = blockDim.x;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps leave; a block-wide row never does
   RawChunk<R> x[NV];
-  if constexpr (CKPT) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float v[kChunk];
-      ckpt_chunk<VEC>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt, i, t, threads,
-                      a.width, v);
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) x[i].v[j] = v[j];
+  for (int i = 0; i < NV; ++i) {
+    if constexpr (CKPT) {
+      x[i] = narrow<R>(ckpt_chunk<VEC>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt,
+                                       i, t, threads, a.width));
+    } else if constexpr (VEC) {
+      const int c = column<true>(i, 0, t, threads);
+      x[i] = RawChunk<R>{};
+      if (c < a.width) x[i] = load_chunk(static_cast<const T*>(a.x) + row * a.ldx + c);
+    } else {
+      x[i] = narrow<R>(any_chunk(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width));
     }
-  } else {
-    RawChunk<T> raw[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      raw[i] = row_chunk<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) x[i].v[j] = Elem<R>::from(Elem<T>::to(raw[i].v[j]));
-    if (a.codes)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float v[kChunk];
-        widen(x[i], v);
-        save_chunk<VEC>(v, a.codes + (int64_t)row * a.width, a.scales + (int64_t)row * a.groups, a.fmt, i, t, threads,
-                        a.width);
-      }
   }
+  if (!CKPT && a.codes)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      save_chunk<R, VEC>(x[i], a.codes + (int64_t)row * a.width, a.scales + (int64_t)row * a.groups, a.fmt, i, t, threads,
+                         a.width);
   const float inv_n = 1.0f / (float)a.width;
   float mu = 0.f;
   if (a.layer) {
-    float s = 0.f;
+    float2 s = both(0.f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const Chunk v = widen<R>(x[i]);
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) s += Elem<R>::to(x[i].v[j]);
-    mu = row_sum2(s, 0.f, threads, 1, buf[0]).x * inv_n;
-  }
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const float d = Elem<R>::to(x[i].v[j]) - mu;
-      if (column<VEC>(i, VEC ? 0 : j, t, threads) < a.width) q += d * d;
+      for (int j = 0; j < kChunk / 2; ++j) s = add2(s, v.p[j]);
     }
-  const float r = 1.0f / sqrtf(row_sum2(q, 0.f, threads, 1, buf[1]).x * inv_n + a.eps);
+    mu = row_sum2(s.x + s.y, 0.f, threads, 1, buf[0]).x * inv_n;
+  }
+  float2 q = both(0.f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float w[kChunk], b[kChunk], v[kChunk];
-    load_vector<VEC>(a.weight, a.w_type, i, t, threads, a.width, 1.f, w);
-    load_vector<VEC>(a.bias, a.w_type, i, t, threads, a.width, 0.f, b);
+    Chunk v = widen<R>(x[i]);
+    if (VEC) {
+      if (column<true>(i, 0, t, threads) < a.width)
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) v[j] = (Elem<R>::to(x[i].v[j]) - mu) * r * w[j] + b[j];
+        for (int j = 0; j < kChunk / 2; ++j) {
+          const float2 d = add2(v.p[j], both(-mu));
+          q = fma2(d, d, q);
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const float d = v[j] - mu;
+        if (column<false>(i, j, t, threads) < a.width) q.x += d * d;
+      }
+    }
+  }
+  const float r = 1.0f / sqrtf(row_sum2(q.x + q.y, 0.f, threads, 1, buf[1]).x * inv_n + a.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (VEC && column<true>(i, 0, t, threads) >= a.width) continue;
+    Chunk v = widen<R>(x[i]);
+#pragma unroll
+    for (int j = 0; j < kChunk / 2; ++j) v.p[j] = mul2(add2(v.p[j], both(-mu)), both(r));
+    if (a.weight) {
+      const Chunk w = load_vector<VEC>(a.weight, a.w_type, i, t, threads, a.width, 1.f);
+#pragma unroll
+      for (int j = 0; j < kChunk / 2; ++j) v.p[j] = mul2(v.p[j], w.p[j]);
+    }
+    if (a.bias) {
+      const Chunk b = load_vector<VEC>(a.bias, a.w_type, i, t, threads, a.width, 0.f);
+#pragma unroll
+      for (int j = 0; j < kChunk / 2; ++j) v.p[j] = add2(v.p[j], b.p[j]);
+    }
     store_row_chunk<T, VEC>(static_cast<T*>(a.y) + (int64_t)row * a.width, i, t, threads, a.width, v);
   }
   if (t == 0) {
@@ -321,16 +320,16 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
     if (VEC) copy_commit();
   };
 
-  float dw[NV][kChunk], db[SUMB ? NV : 1][kChunk], w[NV][kChunk];
+  Chunk dw[NV], db[SUMB ? NV : 1], w[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    fill(dw[i], 0.f);
-    if (SUMB) fill(db[i], 0.f);
+    dw[i] = chunk_of(0.f);
+    if (SUMB) db[i] = chunk_of(0.f);
   }
   const int first = blockIdx.x * blockDim.y + group;
   for (int s = 0; s < a.stages; ++s) fetch(first + s * step, s);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) load_vector<VEC>(a.weight, a.w_type, i, t, threads, a.width, 1.f, w[i]);
+  for (int i = 0; i < NV; ++i) w[i] = load_vector<VEC>(a.weight, a.w_type, i, t, threads, a.width, 1.f);
 
   uint32_t bytes[NV] = {};  // scale bytes of the row at hand
   auto fetch_bytes = [&](int row, uint32_t (&b)[NV]) {
@@ -351,23 +350,21 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
   int stage = 0, turn = 0;
   for (int row = first; row < a.rows; row += step) {
     // x and dy of chunk i; columns past the width give 0 for dy and for w
-    auto chunk = [&](int i, float (&xv)[kChunk], float (&gv)[kChunk]) {
+    auto chunk = [&](int i, Chunk& xv, Chunk& gv) {
       if (VEC) {
+        gv = xv = chunk_of(0.f);
         if (column<true>(i, 0, t, threads) < a.width) {
-          widen(*reinterpret_cast<const RawChunk<T>*>(slot_g(stage, i)), gv);
-          if (CKPT) ckpt_decode8<float>(*reinterpret_cast<const uint2*>(slot_x(stage, i)), bytes[i], a.in_fmt, xv);
-          else widen(*reinterpret_cast<const RawChunk<T>*>(slot_x(stage, i)), xv);
-        } else {
-          fill(gv, 0.f);
-          fill(xv, 0.f);
+          gv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(slot_g(stage, i)));
+          if (CKPT) xv = ckpt_decode8<float>(*reinterpret_cast<const uint2*>(slot_x(stage, i)), bytes[i], a.in_fmt);
+          else xv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(slot_x(stage, i)));
         }
       } else {
-        widen(row_chunk<T, false>(static_cast<const T*>(a.gy) + row * a.ldg, i, t, threads, a.width), gv);
+        gv = any_chunk(static_cast<const T*>(a.gy) + row * a.ldg, i, t, threads, a.width);
         if (CKPT)
-          ckpt_chunk<false>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt, i, t,
-                            threads, a.width, xv);
+          xv = ckpt_chunk<false>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt, i, t,
+                                 threads, a.width);
         else
-          widen(row_chunk<T, false>(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width), xv);
+          xv = any_chunk(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width);
       }
     };
     const int next = row + step;
@@ -380,28 +377,33 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
     fetch_bytes(next, next_bytes);
     if (VEC) copy_wait_but(a.stages - 1);
 
-    float s1 = 0.f, s2 = 0.f;
+    float2 s1 = both(0.f), s2 = both(0.f);
+    const float2 r2 = both(r), off = both(-mu * r);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float xv[kChunk], gv[kChunk];
+      Chunk xv, gv;
       chunk(i, xv, gv);
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const float xh = (xv[j] - mu) * r, p = gv[j] * w[i][j];
-        dw[i][j] += gv[j] * xh;
-        if (SUMB) db[i][j] += gv[j];
-        s1 += p;
-        s2 += p * xh;
+      for (int j = 0; j < kChunk / 2; ++j) {
+        const float2 xh = fma2(xv.p[j], r2, off), p = mul2(gv.p[j], w[i].p[j]);
+        dw[i].p[j] = fma2(gv.p[j], xh, dw[i].p[j]);
+        if (SUMB) db[i].p[j] = add2(db[i].p[j], gv.p[j]);
+        s1 = add2(s1, p);
+        s2 = fma2(p, xh, s2);
       }
     }
-    const float2 s = row_sum2(s1, s2, threads, 1 + group, buf[turn] + warp0);
+    const float2 s = row_sum2(s1.x + s1.y, s2.x + s2.y, threads, 1 + group, buf[turn] + warp0);
     const float m1 = a.layer ? s.x * inv_n : 0.f, m2 = s.y * inv_n;
+    const float2 c0 = both(-r * m1), c1 = both(-r * m2);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float xv[kChunk], gv[kChunk];
+      Chunk xv, gv;
       chunk(i, xv, gv);
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) xv[j] = r * (gv[j] * w[i][j] - m1 - (xv[j] - mu) * r * m2);
+      for (int j = 0; j < kChunk / 2; ++j) {
+        const float2 xh = fma2(xv.p[j], r2, off);
+        xv.p[j] = fma2(mul2(gv.p[j], w[i].p[j]), r2, fma2(xh, c1, c0));
+      }
       store_row_chunk<T, VEC>(static_cast<T*>(a.gx) + (int64_t)row * a.width, i, t, threads, a.width, xv);
     }
     fetch(row + a.stages * step, stage);
@@ -490,8 +492,10 @@ Shape fwd_shape(const NormArgs& a, int type, bool vec) {
   return shape_for(a.width, vec && !a.in_codes && type != RAWINT4_TYPE_F32 ? 8 : 4, kFwdWarps);
 }
 
-Shape bwd_shape(int width) {
-  Shape s = shape_for(width, 4, 1);
+// Backward: 32 registers a thread for each of w, dw and db at four chunks; with
+// db the block takes two chunks a thread where the row's threads then still fit.
+Shape bwd_shape(int width, bool bias) {
+  Shape s = shape_for(width, bias && width <= 2 * kChunk * kBwdThreads ? 2 : 4, 1);
   s.rows = kBwdThreads / s.threads;
   return s;
 }
@@ -509,7 +513,7 @@ int stage_bytes(const Shape& s, int type, bool ckpt) {
 
 template <class T, int NV, bool VEC, bool CKPT, bool SUMB>
 cudaError_t launch_bwd(NormArgs a, int type, cudaStream_t st) {
-  const Shape s = bwd_shape(a.width);
+  const Shape s = bwd_shape(a.width, SUMB);
   const int stage = stage_bytes(s, type, CKPT);
   a.stages = VEC ? kBwdRing / stage : 1;
   if (a.stages > kBwdMaxStages) a.stages = kBwdMaxStages;
@@ -563,7 +567,7 @@ cudaError_t pick_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
 
 template <class T>
 cudaError_t run_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
-  const int nv = bwd_shape(a.width).nv;
+  const int nv = bwd_shape(a.width, a.want_b).nv;
   if (nv == 1) return pick_bwd<T, 1>(a, type, vec, st);
   if (nv == 2) return pick_bwd<T, 2>(a, type, vec, st);
   return pick_bwd<T, 4>(a, type, vec, st);
@@ -671,7 +675,8 @@ RAWINT4_API int rawint4_norm_fwd(const rawint4_norm_cfg* cfg, const void* x, int
 
 RAWINT4_API int rawint4_norm_bwd_workspace_size(const rawint4_norm_cfg* cfg, size_t* bytes) {
   if (!cfg_ok(cfg) || !bytes) return RAWINT4_INVALID_ARGUMENT;
-  const size_t n = (size_t)2 * bwd_blocks(bwd_shape(cfg->width), cfg->rows) * cfg->width * sizeof(float);
+  const size_t blocks = cfg->rows < kBwdBlocks ? cfg->rows : kBwdBlocks;
+  const size_t n = 2 * blocks * cfg->width * sizeof(float);
   *bytes = (n + 255) / 256 * 256;
   return RAWINT4_OK;
 }
@@ -720,7 +725,7 @@ RAWINT4_API int rawint4_norm_bwd(const rawint4_norm_cfg* cfg, const void* x, int
   }
   if (sums) {
     R4_PROF("norm_fold", st);
-    if (launch_fold(a.partial, bwd_blocks(bwd_shape(a.width), a.rows), a.width, grad_weight, grad_bias, cfg->weight_type,
+    if (launch_fold(a.partial, bwd_blocks(bwd_shape(a.width, a.want_b), a.rows), a.width, grad_weight, grad_bias, cfg->weight_type,
                     accumulate, st) != cudaSuccess)
       return RAWINT4_CUDA_ERROR;
   }

@@ -33,19 +33,70 @@ template <>
 struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ float to(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ float2 widen(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t narrow(float2 v) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  }
   static constexpr float kMax = 3.3895313892515355e38f;
 };
 template <>
 struct Elem<__half> {
   static __device__ __forceinline__ float to(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half from(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ float2 widen(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t narrow(float2 v) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
   static constexpr float kMax = 65504.f;
 };
 
-// One chunk as it lies in memory (16 bytes for the 16-bit types, 32 for fp32).
+// Two fp32 operations in one instruction (f32x2), each rounded by itself.
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+  return (uint64_t)__float_as_uint(v.x) | (uint64_t)__float_as_uint(v.y) << 32;
+}
+__device__ __forceinline__ float2 float2_of(uint64_t b) {
+  return make_float2(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// A chunk in fp32, as the pairs the arithmetic works on.
+struct Chunk {
+  float2 p[kChunk / 2];
+  __device__ __forceinline__ float& operator[](int j) { return j & 1 ? p[j / 2].y : p[j / 2].x; }
+  __device__ __forceinline__ float operator[](int j) const { return j & 1 ? p[j / 2].y : p[j / 2].x; }
+};
+__device__ __forceinline__ Chunk chunk_of(float v) {
+  Chunk c;
+#pragma unroll
+  for (int j = 0; j < kChunk / 2; ++j) c.p[j] = both(v);
+  return c;
+}
+
+// A chunk as it lies in memory (16 bytes for the 16-bit types, 32 for fp32).
 template <class T>
 struct alignas(16) RawChunk {
-  T v[kChunk];
+  uint32_t w[kChunk * sizeof(T) / 4];
 };
 
 template <class T>
@@ -59,10 +110,36 @@ __device__ __forceinline__ RawChunk<T> load_chunk(const T* p) {
 }
 
 template <class T>
-__device__ __forceinline__ void store_chunk(T* p, const float (&f)[kChunk]) {
+__device__ __forceinline__ Chunk widen(const RawChunk<T>& r) {
+  Chunk c;
+#pragma unroll
+  for (int j = 0; j < kChunk / 2; ++j) {
+    if constexpr (sizeof(T) == 4)
+      c.p[j] = make_float2(__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1]));
+    else
+      c.p[j] = Elem<T>::widen(r.w[j]);
+  }
+  return c;
+}
+
+template <class T>
+__device__ __forceinline__ RawChunk<T> narrow(const Chunk& c) {
   RawChunk<T> r;
 #pragma unroll
-  for (int i = 0; i < kChunk; ++i) r.v[i] = Elem<T>::from(f[i]);
+  for (int j = 0; j < kChunk / 2; ++j) {
+    if constexpr (sizeof(T) == 4) {
+      r.w[2 * j] = __float_as_uint(c.p[j].x);
+      r.w[2 * j + 1] = __float_as_uint(c.p[j].y);
+    } else {
+      r.w[j] = Elem<T>::narrow(c.p[j]);
+    }
+  }
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store_chunk(T* p, const Chunk& c) {
+  const RawChunk<T> r = narrow<T>(c);
   const uint4* s = reinterpret_cast<const uint4*>(&r);
   uint4* d = reinterpret_cast<uint4*>(p);
 #pragma unroll
@@ -92,10 +169,8 @@ __device__ __forceinline__ uint32_t ckpt_scale_byte(uint32_t amax_bits, int fmt)
 __device__ __forceinline__ float ckpt_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 __device__ __forceinline__ float ckpt_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-__device__ __forceinline__ bool is_finite_bits(uint32_t abs_bits) { return abs_bits < 0x7F800000u; }
-
 __device__ __forceinline__ uint32_t ckpt_code(float x, float inv, int fmt) {
-  const bool finite = is_finite_bits(__float_as_uint(x) & 0x7FFFFFFFu);
+  const bool finite = (__float_as_uint(x) & 0x7FFFFFFFu) < 0x7F800000u;
   const float v = x * inv;
   if (fmt == RAWINT4_CKPT_E4M3)
     return finite ? (uint32_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3) : 0x7Fu;
@@ -104,44 +179,34 @@ __device__ __forceinline__ uint32_t ckpt_code(float x, float inv, int fmt) {
 
 // Eight codes of finite values (INT8: adding 1.5 2^23 leaves the rounded
 // integer in the low mantissa bits).
-__device__ __forceinline__ uint2 ckpt_codes8(const float (&f)[kChunk], float inv, int fmt) {
+__device__ __forceinline__ uint2 ckpt_codes8(const Chunk& f, float inv, int fmt) {
   uint32_t w[2];
   if (fmt == RAWINT4_CKPT_E4M3) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h] * inv, f[4 * h + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi =
-          __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h + 2] * inv, f[4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(f.p[2 * h], both(inv)), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(f.p[2 * h + 1], both(inv)), __NV_SATFINITE, __NV_E4M3);
       w[h] = lo | hi << 16;
     }
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t u[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(fmaf(f[4 * h + j], inv, 12582912.f));  // exact product, one rounding
-      w[h] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+      // an exact product and one rounding
+      const float2 a = fma2(f.p[2 * h], both(inv), both(12582912.f)), b = fma2(f.p[2 * h + 1], both(inv), both(12582912.f));
+      w[h] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                         __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
     }
   }
   return make_uint2(w[0], w[1]);
 }
 
-// The chunk's share of a group's largest magnitude: bits of |x|, infinities
-// and NaN included.
-__device__ __forceinline__ uint32_t abs_bits8(const float (&f)[kChunk]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < kChunk; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-  return m;
-}
-
 // Codes and scale byte of a chunk whose group lies in four neighbouring
 // lanes; called by all lanes of a warp (a lane without a chunk passes zeros).
-__device__ __forceinline__ uint2 ckpt_encode8(const float (&f)[kChunk], int fmt, uint32_t* byte) {
-  uint32_t amax = abs_bits8(f);
+// `amax`: the chunk's largest |x| as fp32 bits, infinities and NaN included.
+__device__ __forceinline__ uint2 ckpt_encode8(const Chunk& f, uint32_t amax, int fmt, uint32_t* byte) {
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  if (__any_sync(0xffffffffu, !is_finite_bits(amax))) {  // rare: leave such values out of the scale, code them as NaN
+  if (__any_sync(0xffffffffu, amax >= 0x7F800000u)) {  // rare: leave such values out of the scale, code them as NaN
     amax = 0;
 #pragma unroll
     for (int j = 0; j < kChunk; ++j) amax = max(amax, finite_abs_bits(f[j]));
@@ -156,6 +221,23 @@ __device__ __forceinline__ uint2 ckpt_encode8(const float (&f)[kChunk], int fmt,
   }
   *byte = ckpt_scale_byte(amax, fmt);
   return ckpt_codes8(f, ckpt_inv_scale(*byte), fmt);
+}
+
+// The chunk's largest |x| as fp32 bits; 16-bit types compare two at a time.
+template <class T>
+__device__ __forceinline__ uint32_t abs_max_bits(const RawChunk<T>& r) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) m = max(m, r.w[j] & 0x7FFFFFFFu);
+    return m;
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kChunk / 2; ++j) m = __vmaxu2(m, r.w[j] & 0x7FFF7FFFu);
+    m = max(m & 0xFFFFu, m >> 16);
+    return __float_as_uint(Elem<T>::widen(m).x);
+  }
 }
 
 // Value of a code; |code| 2^e beyond fp32 gives an infinity.
@@ -183,22 +265,25 @@ __device__ __forceinline__ uint32_t ckpt_safe_byte(int fmt) {
 
 // Eight values of a checkpoint, saturated for type T.
 template <class T>
-__device__ __forceinline__ void ckpt_decode8(uint2 w, uint32_t byte, int fmt, float (&f)[kChunk]) {
-  const float scale = ckpt_scale(byte);
+__device__ __forceinline__ Chunk ckpt_decode8(uint2 w, uint32_t byte, int fmt) {
+  const float2 scale = both(ckpt_scale(byte));
+  Chunk f;
   if (fmt == RAWINT4_CKPT_E4M3) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint32_t two = ((q < 2 ? w.x : w.y) >> (16 * (q & 1))) & 0xFFFFu;
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-      const float2 v = __half22float2(__half2(h));
-      f[2 * q] = v.x * scale;
-      f[2 * q + 1] = v.y * scale;
+      f.p[q] = mul2(__half22float2(__half2(h)), scale);
     }
   } else {
     const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};  // code + 128 in the low bits of 2^23
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j)
-      f[j] = (__uint_as_float(__byte_perm(u[j / 4], 0x4B000000u, 0x7440 + j % 4)) - 8388736.f) * scale;
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t sel = 0x7440 + 2 * (q & 1);
+      const float2 v = make_float2(__uint_as_float(__byte_perm(u[q / 2], 0x4B000000u, sel)),
+                                   __uint_as_float(__byte_perm(u[q / 2], 0x4B000000u, sel + 1)));
+      f.p[q] = mul2(add2(v, both(-8388736.f)), scale);
+    }
     if (__vcmpeq4(w.x, 0x80808080u) | __vcmpeq4(w.y, 0x80808080u)) {
 #pragma unroll
       for (int j = 0; j < kChunk; ++j)
@@ -209,6 +294,7 @@ __device__ __forceinline__ void ckpt_decode8(uint2 w, uint32_t byte, int fmt, fl
 #pragma unroll
     for (int j = 0; j < kChunk; ++j) f[j] = ckpt_saturate(f[j], Elem<T>::kMax);
   }
+  return f;
 }
 
 __device__ __forceinline__ float row_warp_sum(float v) {
