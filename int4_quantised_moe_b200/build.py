@@ -16,8 +16,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librawint4_moe.so")
 SOURCES = ["api.cu", "gemm_pair.cu", "gemm_tm.cu", "gemm_pair_narrow.cu", "gemm_tm_narrow.cu", "skinny.cu", "route.cu",
-           "aux.cu", "prof.cu", "noalloc.cu", "router.cu", "select.cu", "norm.cu", "ckpt8.cu"]
-HEADERS = ["common.cuh", "gemm.cuh", "skinny.cuh", "route.cuh", "aux.cuh", "prof.cuh", "router.cuh", "rows.cuh"]
+           "aux.cu", "prof.cu", "noalloc.cu", "router.cu", "select.cu", "select_f32.cu", "select_bf16.cu",
+           "select_f16.cu", "norm.cu", "ckpt8.cu"]
+HEADERS = ["common.cuh", "gemm.cuh", "skinny.cuh", "route.cuh", "aux.cuh", "prof.cuh", "router.cuh", "rows.cuh", "select.cuh", "select_kernels.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

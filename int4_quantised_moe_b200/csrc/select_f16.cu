@@ -1,0 +1,15 @@
+// Expert selection for scores of one type (the types compile in parallel).
+#include "select_kernels.cuh"
+
+namespace r4 {
+
+template <>
+cudaError_t run_select<__half>(const SelectArgs& a, int sms, cudaStream_t st) {
+  return select_type<__half>(a, sms, st);
+}
+template <>
+cudaError_t run_select_bwd<__half>(const SelectArgs& a, cudaStream_t st) {
+  return select_bwd_type<__half>(a, st);
+}
+
+}  // namespace r4
