@@ -476,9 +476,11 @@ def router_bwd(scores: torch.Tensor, ids: torch.Tensor, grad_route: torch.Tensor
 # ---------------------------------------------------------------------------
 # Around the layer: expert selection, 8-bit activation checkpoints, norm
 # ---------------------------------------------------------------------------
-# Every call runs on the device of its tensors. `stream` defaults to that
-# device's current stream; results and scratch are allocated on the stream
-# that the call runs on.
+# Every call runs on the device of its tensors, on `stream` or that device's
+# current stream. Results and scratch are allocated on the stream that the call
+# runs on; tensors passed to a call on another stream are recorded there, so
+# they may be dropped at once. Using a result on a third stream is ordered by
+# the caller, as with any torch operation.
 
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -487,37 +489,27 @@ NORM_KINDS = {"layer": 0, "rms": 1}
 CKPT_GROUP = 32  # columns under one scale of a checkpoint
 
 
-class _On:
-    """The device and stream of a call: enters the tensors' device, and the given stream when there
-    is one, so that torch allocates there; yields the raw stream handle."""
+def _elsewhere(device: torch.device, stream, *tensors):
+    """The context in which a call has to be made again, or None when it can run right here: on the
+    current device and its current stream."""
+    if stream is None:
+        return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    for t in tensors:
+        if isinstance(t, Ckpt8):
+            t.codes.record_stream(stream)
+            t.scales.record_stream(stream)
+        elif t is not None:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
 
-    __slots__ = ("device", "stream", "guards")
 
-    def __init__(self, device: torch.device, stream):
-        self.device, self.stream, self.guards = device, stream, ()
-
-    def __enter__(self) -> int:
-        index = self.device.index
-        if self.stream is None:
-            if index != torch.cuda.current_device():
-                guard = torch.cuda.device(index)
-                guard.__enter__()
-                self.guards = (guard,)
-            return torch.cuda.current_stream(index).cuda_stream
-        s = self.stream
-        if not isinstance(s, torch.cuda.Stream):
-            s = torch.cuda.ExternalStream(int(s), device=self.device)
-        if s.device != self.device:
-            raise ValueError(f"the stream is on {s.device}, the tensors are on {self.device}")
-        guard = torch.cuda.stream(s)
-        guard.__enter__()
-        self.guards = (guard,)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        for g in self.guards:
-            g.__exit__(*exc)
-        return False
+def _here(device: torch.device) -> int:
+    """Handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _choice(table: dict, value, name: str) -> int:
@@ -575,13 +567,17 @@ def router_select(scores: torch.Tensor, cfg: SelectCfg, bias: Optional[torch.Ten
         _expect(bias, "bias", torch.float32, (E,), dev)
     if counts is not None:
         _expect(counts, "counts", torch.int32, (E,), dev)
+    ctx = _elsewhere(dev, stream, scores, bias, counts)
+    if ctx is not None:
+        with ctx:
+            return router_select(scores, cfg, bias, counts)
     q = scores.shape[0]
-    with _On(dev, stream) as st:
-        ids = torch.empty((q, cfg.top_k), dtype=torch.int64, device=dev)
-        w = torch.empty((q, cfg.top_k), dtype=torch.float32, device=dev)
-        _check(_lib.rawint4_moe_router_select(_typed(cfg, scores.dtype), scores.data_ptr(), pitch, q, _ptr(bias),
-                                              ids.data_ptr(), w.data_ptr(), _ptr(counts), st),
-               "rawint4_moe_router_select")
+    ids = scores.new_empty((q, cfg.top_k), dtype=torch.int64)
+    w = scores.new_empty((q, cfg.top_k), dtype=torch.float32)
+    _check(_lib.rawint4_moe_router_select(_typed(cfg, scores.dtype), scores.data_ptr(), pitch, q,
+                                          None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(),
+                                          None if counts is None else counts.data_ptr(), _here(dev)),
+           "rawint4_moe_router_select")
     return ids, w
 
 
@@ -593,11 +589,14 @@ def router_select_bwd(scores: torch.Tensor, cfg: SelectCfg, ids: torch.Tensor, g
     q = scores.shape[0]
     _expect(ids, "ids", torch.int64, (q, cfg.top_k), dev)
     _expect(grad_route, "grad_route", torch.float32, (q, cfg.top_k), dev)
-    with _On(dev, stream) as st:
-        grad = torch.empty((q, cfg.experts), dtype=scores.dtype, device=dev)
-        _check(_lib.rawint4_moe_router_select_bwd(_typed(cfg, scores.dtype), scores.data_ptr(), pitch, q, ids.data_ptr(),
-                                                  grad_route.data_ptr(), grad.data_ptr(), st),
-               "rawint4_moe_router_select_bwd")
+    ctx = _elsewhere(dev, stream, scores, ids, grad_route)
+    if ctx is not None:
+        with ctx:
+            return router_select_bwd(scores, cfg, ids, grad_route)
+    grad = scores.new_empty((q, cfg.experts))
+    _check(_lib.rawint4_moe_router_select_bwd(_typed(cfg, scores.dtype), scores.data_ptr(), pitch, q, ids.data_ptr(),
+                                              grad_route.data_ptr(), grad.data_ptr(), _here(dev)),
+           "rawint4_moe_router_select_bwd")
     return grad
 
 
@@ -626,20 +625,24 @@ class Ckpt8:
         return fmt
 
 
-def _empty_ckpt8(rows: int, width: int, fmt: str, device) -> Ckpt8:
-    return Ckpt8(torch.empty((rows, width), dtype=torch.uint8, device=device),
-                 torch.empty((rows, -(-width // CKPT_GROUP)), dtype=torch.uint8, device=device), fmt)
+def _empty_ckpt8(x: torch.Tensor, fmt: str) -> Ckpt8:
+    rows, width = x.shape
+    return Ckpt8(x.new_empty((rows, width), dtype=torch.uint8),
+                 x.new_empty((rows, -(-width // CKPT_GROUP)), dtype=torch.uint8), fmt)
 
 
 def ckpt8_save(x: torch.Tensor, format: str = "e4m3", stream=None) -> Ckpt8:
     """x [rows, width] (fp32, bf16 or fp16) in 8 bits; see include/rawint4_moe.h for the format."""
     fmt = _choice(CKPT_FORMATS, format, "format")
     pitch = _rows(x, "x")
+    ctx = _elsewhere(x.device, stream, x)
+    if ctx is not None:
+        with ctx:
+            return ckpt8_save(x, format)
     rows, width = x.shape
-    with _On(x.device, stream) as st:
-        out = _empty_ckpt8(rows, width, format, x.device)
-        _check(_lib.rawint4_ckpt8_save(fmt, TYPES[x.dtype], x.data_ptr(), pitch, rows, width, out.codes.data_ptr(),
-                                       out.scales.data_ptr(), st), "rawint4_ckpt8_save")
+    out = _empty_ckpt8(x, format)
+    _check(_lib.rawint4_ckpt8_save(fmt, TYPES[x.dtype], x.data_ptr(), pitch, rows, width, out.codes.data_ptr(),
+                                   out.scales.data_ptr(), _here(x.device)), "rawint4_ckpt8_save")
     return out
 
 
@@ -648,11 +651,14 @@ def ckpt8_load(ckpt: Ckpt8, dtype: torch.dtype = torch.bfloat16, stream=None) ->
     fmt = ckpt.check("ckpt")
     typ = _choice(TYPES, dtype, "dtype")
     codes = ckpt.codes
+    ctx = _elsewhere(codes.device, stream, ckpt)
+    if ctx is not None:
+        with ctx:
+            return ckpt8_load(ckpt, dtype)
     rows, width = codes.shape
-    with _On(codes.device, stream) as st:
-        out = torch.empty((rows, width), dtype=dtype, device=codes.device)
-        _check(_lib.rawint4_ckpt8_load(fmt, codes.data_ptr(), ckpt.scales.data_ptr(), rows, width, typ, out.data_ptr(),
-                                       st), "rawint4_ckpt8_load")
+    out = codes.new_empty((rows, width), dtype=dtype)
+    _check(_lib.rawint4_ckpt8_load(fmt, codes.data_ptr(), ckpt.scales.data_ptr(), rows, width, typ, out.data_ptr(),
+                                   _here(codes.device)), "rawint4_ckpt8_load")
     return out
 
 
@@ -698,15 +704,19 @@ def norm_fwd(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tens
             wdtype = bias.dtype
         _vector(bias, "bias", width, dev)
         _expect(bias, "bias", wdtype, (width,), dev)
-    with _On(dev, stream) as st:
-        y = torch.empty((rows, width), dtype=dtype, device=dev)
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        mean = torch.empty(rows, dtype=torch.float32, device=dev) if kind == "layer" else None
-        out = None if save is None else _empty_ckpt8(rows, width, save, dev)
-        _check(_lib.rawint4_norm_fwd(NormCfg(rows, width, k, typ, TYPES[wdtype], eps), ptr, pitch, ck, _ptr(weight),
-                                     _ptr(bias), y.data_ptr(), _ptr(mean), rstd.data_ptr(), fmt,
-                                     None if out is None else out.codes.data_ptr(),
-                                     None if out is None else out.scales.data_ptr(), st), "rawint4_norm_fwd")
+    ctx = _elsewhere(dev, stream, x, weight, bias)
+    if ctx is not None:
+        with ctx:
+            return norm_fwd(x, weight, bias, kind, eps, dtype, save)
+    like = x if ck is None else x.codes
+    y = like.new_empty((rows, width), dtype=dtype)
+    rstd = like.new_empty(rows, dtype=torch.float32)
+    mean = like.new_empty(rows, dtype=torch.float32) if kind == "layer" else None
+    out = None if save is None else _empty_ckpt8(x, save)
+    _check(_lib.rawint4_norm_fwd(NormCfg(rows, width, k, typ, TYPES[wdtype], eps), ptr, pitch, ck, _ptr(weight),
+                                 _ptr(bias), y.data_ptr(), _ptr(mean), rstd.data_ptr(), fmt,
+                                 None if out is None else out.codes.data_ptr(),
+                                 None if out is None else out.scales.data_ptr(), _here(dev)), "rawint4_norm_fwd")
     return y, mean, rstd, out
 
 
@@ -743,22 +753,25 @@ def norm_bwd(grad_y: torch.Tensor, x, rstd: torch.Tensor, weight: Optional[torch
         _expect(grad_weight, "grad_weight", wdtype, (width,), dev)
     if grad_bias is not None:
         _expect(grad_bias, "grad_bias", wdtype, (width,), dev)
-    with _On(dev, stream) as st:
-        grad_x = torch.empty((rows, width), dtype=dtype, device=dev)
-        if weight is not None and grad_weight is None:
-            grad_weight = torch.empty(width, dtype=wdtype, device=dev)
-        if bias_grad and grad_bias is None:
-            grad_bias = torch.empty(width, dtype=wdtype, device=dev)
-        cfg = NormCfg(rows, width, k, TYPES[dtype], TYPES[wdtype], 1.0)  # eps is in rstd already
-        ws, nbytes = None, 0
-        if grad_weight is not None or grad_bias is not None:
-            n = ctypes.c_size_t(0)
-            _check(_lib.rawint4_norm_bwd_workspace_size(cfg, n), "rawint4_norm_bwd_workspace_size")
-            nbytes = n.value
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(_lib.rawint4_norm_bwd(cfg, ptr, pitch, ck, grad_y.data_ptr(), gpitch, _ptr(weight), _ptr(mean),
-                                     rstd.data_ptr(), grad_x.data_ptr(), _ptr(grad_weight), _ptr(grad_bias),
-                                     1 if accumulate else 0, _ptr(ws), nbytes, st), "rawint4_norm_bwd")
+    ctx = _elsewhere(dev, stream, grad_y, x, rstd, weight, mean, grad_weight, grad_bias)
+    if ctx is not None:
+        with ctx:
+            return norm_bwd(grad_y, x, rstd, weight, mean, kind, bias_grad, grad_weight, grad_bias, accumulate)
+    grad_x = grad_y.new_empty((rows, width))
+    if weight is not None and grad_weight is None:
+        grad_weight = grad_y.new_empty(width, dtype=wdtype)
+    if bias_grad and grad_bias is None:
+        grad_bias = grad_y.new_empty(width, dtype=wdtype)
+    cfg = NormCfg(rows, width, k, TYPES[dtype], TYPES[wdtype], 1.0)  # eps is in rstd already
+    ws, nbytes = None, 0
+    if grad_weight is not None or grad_bias is not None:
+        n = ctypes.c_size_t(0)
+        _check(_lib.rawint4_norm_bwd_workspace_size(cfg, n), "rawint4_norm_bwd_workspace_size")
+        nbytes = n.value
+        ws = grad_y.new_empty(nbytes, dtype=torch.uint8)
+    _check(_lib.rawint4_norm_bwd(cfg, ptr, pitch, ck, grad_y.data_ptr(), gpitch, _ptr(weight), _ptr(mean),
+                                 rstd.data_ptr(), grad_x.data_ptr(), _ptr(grad_weight), _ptr(grad_bias),
+                                 1 if accumulate else 0, _ptr(ws), nbytes, _here(dev)), "rawint4_norm_bwd")
     return grad_x, grad_weight, grad_bias
 
 

@@ -294,30 +294,43 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // slots of this thread: [stage][chunk][thread], x behind dy
-  const int all = threads * blockDim.y, me = group * threads + t;
-  auto slot_g = [&](int stage, int i) { return ring + ((int64_t)(stage * NV + i) * all + me) * sizeof(RawChunk<T>); };
-  uint8_t* const ring_x = ring + (int64_t)a.stages * NV * all * sizeof(RawChunk<T>);
-  auto slot_x = [&](int stage, int i) { return ring_x + ((int64_t)(stage * NV + i) * all + me) * kXBytes; };
-  auto fetch = [&](int row, int stage) {
-    if (VEC && row < a.rows) {
+  constexpr int kG = (int)sizeof(RawChunk<T>);
+  const int all = threads * blockDim.y;
+  uint8_t* const my_g = ring + (group * threads + t) * kG;
+  uint8_t* const my_x = ring + a.stages * NV * all * kG + (group * threads + t) * kXBytes;
+  // offsets of chunk 0 of the stage at hand; chunks lie all * size apart
+  int at_g = 0, at_x = 0;
+  const int step_g = all * kG, step_x = all * kXBytes;
+  bool in[NV];  // the thread's chunks that the row has
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = column<true>(i, 0, t, threads);
-        if (c < a.width) {
-          const T* g = static_cast<const T*>(a.gy) + row * a.ldg + c;
-          copy_async16(slot_g(stage, i), g);
-          if (sizeof(T) == 4) copy_async16(slot_g(stage, i) + 16, g + 4);
+  for (int i = 0; i < NV; ++i) in[i] = column<VEC>(i, 0, t, threads) < a.width;
+  auto fetch = [&](int row) {
+    if (VEC && row < a.rows) {
+      const T* g = static_cast<const T*>(a.gy) + row * a.ldg + t * kChunk;
+      const T* x = static_cast<const T*>(a.x) + row * a.ldx + t * kChunk;
+      const uint8_t* codes = a.in_codes + (int64_t)row * a.width + t * kChunk;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (in[i]) {
+          const int c = i * threads * kChunk;
+          uint8_t* const sg = my_g + at_g + i * step_g;
+          uint8_t* const sx = my_x + at_x + i * step_x;
+          copy_async16(sg, g + c);
+          if (sizeof(T) == 4) copy_async16(sg + 16, g + c + 4);
           if (CKPT) {
-            copy_async8(slot_x(stage, i), a.in_codes + (int64_t)row * a.width + c);
+            copy_async8(sx, codes + c);
           } else {
-            const T* x = static_cast<const T*>(a.x) + row * a.ldx + c;
-            copy_async16(slot_x(stage, i), x);
-            if (sizeof(T) == 4) copy_async16(slot_x(stage, i) + 16, x + 4);
+            copy_async16(sx, x + c);
+            if (sizeof(T) == 4) copy_async16(sx + 16, x + c + 4);
           }
         }
-      }
     }
     if (VEC) copy_commit();
+  };
+  auto next_stage = [&] {
+    at_g += NV * step_g;
+    at_x += NV * step_x;
+    if (at_g == a.stages * NV * step_g) at_g = at_x = 0;
   };
 
   Chunk dw[NV], db[SUMB ? NV : 1], w[NV];
@@ -327,7 +340,10 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
     if (SUMB) db[i] = chunk_of(0.f);
   }
   const int first = blockIdx.x * blockDim.y + group;
-  for (int s = 0; s < a.stages; ++s) fetch(first + s * step, s);
+  for (int s = 0; s < a.stages; ++s) {
+    fetch(first + s * step);
+    next_stage();
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) w[i] = load_vector<VEC>(a.weight, a.w_type, i, t, threads, a.width, 1.f);
 
@@ -335,10 +351,8 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
   auto fetch_bytes = [&](int row, uint32_t (&b)[NV]) {
     if (CKPT && VEC && row < a.rows)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = column<true>(i, 0, t, threads);
-        if (c < a.width) b[i] = a.in_scales[(int64_t)row * a.groups + c / kCkptGroup];
-      }
+      for (int i = 0; i < NV; ++i)
+        if (in[i]) b[i] = a.in_scales[(int64_t)row * a.groups + column<true>(i, 0, t, threads) / kCkptGroup];
   };
   fetch_bytes(first, bytes);
   float r = 0.f, mu = 0.f;
@@ -347,17 +361,16 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
     if (a.layer) mu = a.mean_in[first];
   }
 
-  int stage = 0, turn = 0;
+  int turn = 0;
   for (int row = first; row < a.rows; row += step) {
-    // x and dy of chunk i; columns past the width give 0 for dy and for w
+    // x and dy of a chunk that the row has; in the scalar layout, columns past the width give 0
     auto chunk = [&](int i, Chunk& xv, Chunk& gv) {
       if (VEC) {
-        gv = xv = chunk_of(0.f);
-        if (column<true>(i, 0, t, threads) < a.width) {
-          gv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(slot_g(stage, i)));
-          if (CKPT) xv = ckpt_decode8<float>(*reinterpret_cast<const uint2*>(slot_x(stage, i)), bytes[i], a.in_fmt);
-          else xv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(slot_x(stage, i)));
-        }
+        gv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(my_g + at_g + i * step_g));
+        if (CKPT)
+          xv = ckpt_decode8<float>(*reinterpret_cast<const uint2*>(my_x + at_x + i * step_x), bytes[i], a.in_fmt);
+        else
+          xv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(my_x + at_x + i * step_x));
       } else {
         gv = any_chunk(static_cast<const T*>(a.gy) + row * a.ldg, i, t, threads, a.width);
         if (CKPT)
@@ -381,6 +394,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
     const float2 r2 = both(r), off = both(-mu * r);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      if (!in[i]) continue;
       Chunk xv, gv;
       chunk(i, xv, gv);
 #pragma unroll
@@ -397,6 +411,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
     const float2 c0 = both(-r * m1), c1 = both(-r * m2);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      if (!in[i]) continue;
       Chunk xv, gv;
       chunk(i, xv, gv);
 #pragma unroll
@@ -406,8 +421,8 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
       }
       store_row_chunk<T, VEC>(static_cast<T*>(a.gx) + (int64_t)row * a.width, i, t, threads, a.width, xv);
     }
-    fetch(row + a.stages * step, stage);
-    stage = stage + 1 == a.stages ? 0 : stage + 1;
+    fetch(row + a.stages * step);
+    next_stage();
     turn ^= 1;
     r = next_r;
     mu = next_mu;
