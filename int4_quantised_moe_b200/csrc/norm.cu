@@ -25,8 +25,13 @@ namespace r4 {
 namespace {
 
 constexpr int kMaxWidth = 16384;
+constexpr int kFewRows = 296;        // two rows an SM
 constexpr int kFwdWarps = 8;         // rows of a forward block when a row lies in one warp
-constexpr int kBwdThreads = 512;     // threads of a backward block at most
+// Threads of a backward block at most, so that w, dw and db (8 registers a
+// chunk each) and a checkpoint's numbers (4) fit.
+__host__ __device__ constexpr int bwd_threads(int nv, bool bias, bool ckpt) {
+  return nv == 4 ? 512 : nv == 2 && bias ? (ckpt ? 576 : 640) : 896;
+}
 constexpr int kBwdBlocks = 148;      // blocks of the backward at most, one an SM: rows of partial sums
 constexpr int kBwdMaxStages = 4;     // rows in a thread group's ring
 constexpr int kBwdRing = 200 * 1024; // bytes of shared memory for the rings
@@ -100,15 +105,9 @@ __device__ __forceinline__ Chunk any_chunk(const T* row, int i, int t, int threa
   return v;
 }
 
-// Chunk i of a checkpointed row; values past fp32 saturate.
-template <bool VEC>
-__device__ __forceinline__ Chunk ckpt_chunk(const uint8_t* codes, const uint8_t* scales, int fmt, int i, int t, int threads,
-                                            int width) {
-  if (VEC) {
-    const int c = column<true>(i, 0, t, threads);
-    return c < width ? ckpt_decode8<float>(*reinterpret_cast<const uint2*>(codes + c), scales[c / kCkptGroup], fmt)
-                     : chunk_of(0.f);
-  }
+// Chunk i of a checkpointed row in the scalar layout.
+__device__ __forceinline__ Chunk any_ckpt_chunk(const uint8_t* codes, const uint8_t* scales, int fmt, int i, int t,
+                                                int threads, int width) {
   Chunk v;
 #pragma unroll
   for (int j = 0; j < kChunk; ++j) {
@@ -118,17 +117,12 @@ __device__ __forceinline__ Chunk ckpt_chunk(const uint8_t* codes, const uint8_t*
   return v;
 }
 
-template <class T, bool VEC>
-__device__ __forceinline__ void store_row_chunk(T* row, int i, int t, int threads, int width, const Chunk& v) {
-  if (VEC) {
-    const int c = column<true>(i, 0, t, threads);
-    if (c < width) store_chunk(row + c, v);
-  } else {
+template <class T>
+__device__ __forceinline__ void store_any_chunk(T* row, int i, int t, int threads, int width, const Chunk& v) {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const int c = column<false>(i, j, t, threads);
-      if (c < width) row[c] = Elem<T>::from(v[j]);
-    }
+  for (int j = 0; j < kChunk; ++j) {
+    const int c = column<false>(i, j, t, threads);
+    if (c < width) row[c] = Elem<T>::from(v[j]);
   }
 }
 
@@ -158,99 +152,147 @@ __device__ __forceinline__ void save_chunk(const RawChunk<R>& raw, uint8_t* code
   }
 }
 
-// Sum over the `threads` threads of a row: one warp, or several that meet at
+// Sums over the `threads` threads of a row: one warp, or several that meet at
 // the named barrier `bar` (each sum has its own `buf`, or the callers alternate
 // between two).
+__device__ __forceinline__ void row_barrier(int bar, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+}
+__device__ __forceinline__ float row_sum(float a, int threads, int bar, float* buf) {
+  a = row_warp_sum(a);
+  if (threads == 32) return a;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) buf[threadIdx.x >> 5] = a;
+  row_barrier(bar, threads);
+  return row_warp_sum(lane < threads >> 5 ? buf[lane] : 0.f);
+}
 __device__ __forceinline__ float2 row_sum2(float a, float b, int threads, int bar, float2* buf) {
   a = row_warp_sum(a);
   b = row_warp_sum(b);
   if (threads == 32) return make_float2(a, b);
-  const int lane = threadIdx.x & 31, warps = threads >> 5;
+  const int lane = threadIdx.x & 31;
   if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
-  const float2 v = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
+  row_barrier(bar, threads);
+  const float2 v = lane < threads >> 5 ? buf[lane] : make_float2(0.f, 0.f);
   return make_float2(row_warp_sum(v.x), row_warp_sum(v.y));
 }
 
 // ------------------------------------------------------------------ forward
 // blockDim = (threads of a row, rows): the threads of a row are a warp when
-// blockDim.y > 1, else the block. R is how a row waits in registers: as it
-// came (16-bit types in the vector layout), else as fp32.
+// blockDim.y > 1, else the block. R is how a row waits in registers: in the
+// vector layout as it came (16-bit elements, or a checkpoint's numbers in fp16
+// with a scale a chunk), else as fp32.
 template <class T, class R, int NV, bool VEC, bool CKPT>
-__global__ void __launch_bounds__(512, 2) norm_fwd_kernel(const NormArgs a) {
-  __shared__ float2 buf[2][16];
+__global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormArgs a) {
+  __shared__ float buf[2][16];
+  constexpr bool kScaled = VEC && CKPT;
   const int t = threadIdx.x, threads = blockDim.x;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps leave; a block-wide row never does
+  const int stride = threads * kChunk;  // from a thread's chunk to its next one, in the vector layout
+  bool in[NV];
   RawChunk<R> x[NV];
+  float scale[kScaled ? NV : 1];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if constexpr (CKPT) {
-      x[i] = narrow<R>(ckpt_chunk<VEC>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt,
-                                       i, t, threads, a.width));
+    in[i] = column<VEC>(i, 0, t, threads) < a.width;
+    if constexpr (kScaled) {
+      uint2 codes = make_uint2(0u, 0u);
+      scale[i] = 0.f;
+      if (in[i]) {
+        codes = *reinterpret_cast<const uint2*>(a.in_codes + (int64_t)row * a.width + t * kChunk + i * stride);
+        scale[i] = ckpt_scale(a.in_scales[(int64_t)row * a.groups + (t * kChunk + i * stride) / kCkptGroup]);
+      }
+      x[i].w[0] = codes.x;  // decoded once all loads are on their way
+      x[i].w[1] = codes.y;
+    } else if constexpr (CKPT) {
+      x[i] = narrow<R>(any_ckpt_chunk(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt,
+                                      i, t, threads, a.width));
     } else if constexpr (VEC) {
-      const int c = column<true>(i, 0, t, threads);
       x[i] = RawChunk<R>{};
-      if (c < a.width) x[i] = load_chunk(static_cast<const T*>(a.x) + row * a.ldx + c);
+      if (in[i]) x[i] = load_chunk(static_cast<const T*>(a.x) + row * a.ldx + t * kChunk + i * stride);
     } else {
       x[i] = narrow<R>(any_chunk(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width));
     }
+  }
+  if constexpr (kScaled) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = ckpt_numbers8(make_uint2(x[i].w[0], x[i].w[1]), a.in_fmt);
   }
   if (!CKPT && a.codes)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       save_chunk<R, VEC>(x[i], a.codes + (int64_t)row * a.width, a.scales + (int64_t)row * a.groups, a.fmt, i, t, threads,
                          a.width);
+
   const float inv_n = 1.0f / (float)a.width;
   float mu = 0.f;
+  float2 q = both(0.f);
   if (a.layer) {
     float2 s = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const Chunk v = widen<R>(x[i]);
 #pragma unroll
-      for (int j = 0; j < kChunk / 2; ++j) s = add2(s, v.p[j]);
+      for (int j = 0; j < kChunk / 2; ++j) s = kScaled ? fma2(v.p[j], both(scale[kScaled ? i : 0]), s) : add2(s, v.p[j]);
     }
-    mu = row_sum2(s.x + s.y, 0.f, threads, 1, buf[0]).x * inv_n;
+    mu = row_sum(s.x + s.y, threads, 1, buf[0]) * inv_n;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (VEC && !in[i]) continue;
+      Chunk d = widen<R>(x[i]);
+#pragma unroll
+      for (int j = 0; j < kChunk / 2; ++j)
+        d.p[j] = kScaled ? fma2(d.p[j], both(scale[kScaled ? i : 0]), both(-mu)) : add2(d.p[j], both(-mu));
+      if (!VEC)
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j)
+          if (column<false>(i, j, t, threads) >= a.width) d[j] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kChunk / 2; ++j) q = fma2(d.p[j], d.p[j], q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Chunk v = widen<R>(x[i]);
+      float2 s = kScaled ? both(0.f) : q;
+#pragma unroll
+      for (int j = 0; j < kChunk / 2; ++j) s = fma2(v.p[j], v.p[j], s);
+      q = kScaled ? fma2(mul2(s, both(scale[kScaled ? i : 0])), both(scale[kScaled ? i : 0]), q) : s;
+    }
   }
-  float2 q = both(0.f);
+  const float r = 1.0f / sqrtf(row_sum(q.x + q.y, threads, 1, buf[1]) * inv_n + a.eps);
+  const float2 off = both(-mu * r);
+  T* const y = static_cast<T*>(a.y) + (int64_t)row * a.width;
+  // y of chunk i, given the weight's and bias's tensor type
+  auto finish = [&](auto wt) {
+    using W = decltype(wt);
+    const W* const w = static_cast<const W*>(a.weight);
+    const W* const b = static_cast<const W*>(a.bias);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    Chunk v = widen<R>(x[i]);
-    if (VEC) {
-      if (column<true>(i, 0, t, threads) < a.width)
+    for (int i = 0; i < NV; ++i) {
+      if (VEC && !in[i]) continue;
+      Chunk v = widen<R>(x[i]);
+      const float2 rx = both(kScaled ? r * scale[kScaled ? i : 0] : r);
 #pragma unroll
-        for (int j = 0; j < kChunk / 2; ++j) {
-          const float2 d = add2(v.p[j], both(-mu));
-          q = fma2(d, d, q);
-        }
-    } else {
+      for (int j = 0; j < kChunk / 2; ++j) v.p[j] = fma2(v.p[j], rx, off);
+      if (w) {
+        const Chunk f = VEC ? widen<W>(load_chunk(w + t * kChunk + i * stride)) : any_chunk(w, i, t, threads, a.width);
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const float d = v[j] - mu;
-        if (column<false>(i, j, t, threads) < a.width) q.x += d * d;
+        for (int j = 0; j < kChunk / 2; ++j) v.p[j] = mul2(v.p[j], f.p[j]);
       }
+      if (b) {
+        const Chunk f = VEC ? widen<W>(load_chunk(b + t * kChunk + i * stride)) : any_chunk(b, i, t, threads, a.width);
+#pragma unroll
+        for (int j = 0; j < kChunk / 2; ++j) v.p[j] = add2(v.p[j], f.p[j]);
+      }
+      if (VEC) store_chunk(y + t * kChunk + i * stride, v);
+      else store_any_chunk(y, i, t, threads, a.width, v);
     }
-  }
-  const float r = 1.0f / sqrtf(row_sum2(q.x + q.y, 0.f, threads, 1, buf[1]).x * inv_n + a.eps);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (VEC && column<true>(i, 0, t, threads) >= a.width) continue;
-    Chunk v = widen<R>(x[i]);
-#pragma unroll
-    for (int j = 0; j < kChunk / 2; ++j) v.p[j] = mul2(add2(v.p[j], both(-mu)), both(r));
-    if (a.weight) {
-      const Chunk w = load_vector<VEC>(a.weight, a.w_type, i, t, threads, a.width, 1.f);
-#pragma unroll
-      for (int j = 0; j < kChunk / 2; ++j) v.p[j] = mul2(v.p[j], w.p[j]);
-    }
-    if (a.bias) {
-      const Chunk b = load_vector<VEC>(a.bias, a.w_type, i, t, threads, a.width, 0.f);
-#pragma unroll
-      for (int j = 0; j < kChunk / 2; ++j) v.p[j] = add2(v.p[j], b.p[j]);
-    }
-    store_row_chunk<T, VEC>(static_cast<T*>(a.y) + (int64_t)row * a.width, i, t, threads, a.width, v);
-  }
+  };
+  if (a.w_type == RAWINT4_TYPE_F32) finish(float());
+  else if (a.w_type == RAWINT4_TYPE_BF16) finish(__nv_bfloat16());
+  else finish(__half());
   if (t == 0) {
     if (a.mean) a.mean[row] = mu;
     a.rstd[row] = r;
@@ -283,8 +325,8 @@ __device__ __forceinline__ void copy_wait_but(int n) {
 // dx; otherwise both reads go to memory (the second finds the row in cache).
 // The scale bytes of a checkpoint are fetched one row ahead into registers.
 template <class T, int NV, bool VEC, bool CKPT, bool SUMB>
-__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a) {
-  __shared__ float2 buf[2][16];
+__global__ void __launch_bounds__(bwd_threads(NV, SUMB, CKPT)) norm_bwd_kernel(const NormArgs a) {
+  __shared__ float2 buf[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kXBytes = CKPT ? kChunk : (int)sizeof(RawChunk<T>);
   const int t = threadIdx.x, threads = blockDim.x, group = threadIdx.y;
@@ -363,19 +405,18 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
 
   int turn = 0;
   for (int row = first; row < a.rows; row += step) {
+    RawChunk<__half> numbers[CKPT && VEC ? NV : 1];  // a checkpoint's, decoded once; its scale goes into the factor of xh
     // x and dy of a chunk that the row has; in the scalar layout, columns past the width give 0
     auto chunk = [&](int i, Chunk& xv, Chunk& gv) {
       if (VEC) {
         gv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(my_g + at_g + i * step_g));
-        if (CKPT)
-          xv = ckpt_decode8<float>(*reinterpret_cast<const uint2*>(my_x + at_x + i * step_x), bytes[i], a.in_fmt);
-        else
-          xv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(my_x + at_x + i * step_x));
+        if (CKPT) xv = widen<__half>(numbers[CKPT ? i : 0]);
+        else xv = widen<T>(*reinterpret_cast<const RawChunk<T>*>(my_x + at_x + i * step_x));
       } else {
         gv = any_chunk(static_cast<const T*>(a.gy) + row * a.ldg, i, t, threads, a.width);
         if (CKPT)
-          xv = ckpt_chunk<false>(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt, i, t,
-                                 threads, a.width);
+          xv = any_ckpt_chunk(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, a.in_fmt, i, t,
+                              threads, a.width);
         else
           xv = any_chunk(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width);
       }
@@ -392,14 +433,17 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
 
     float2 s1 = both(0.f), s2 = both(0.f);
     const float2 r2 = both(r), off = both(-mu * r);
+    auto factor = [&](int i) { return CKPT && VEC ? both(r * ckpt_scale(bytes[i])) : r2; };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
       Chunk xv, gv;
+      if (CKPT && VEC) numbers[CKPT && VEC ? i : 0] = ckpt_numbers8(*reinterpret_cast<const uint2*>(my_x + at_x + i * step_x), a.in_fmt);
       chunk(i, xv, gv);
+      const float2 rx = factor(i);
 #pragma unroll
       for (int j = 0; j < kChunk / 2; ++j) {
-        const float2 xh = fma2(xv.p[j], r2, off), p = mul2(gv.p[j], w[i].p[j]);
+        const float2 xh = fma2(xv.p[j], rx, off), p = mul2(gv.p[j], w[i].p[j]);
         dw[i].p[j] = fma2(gv.p[j], xh, dw[i].p[j]);
         if (SUMB) db[i].p[j] = add2(db[i].p[j], gv.p[j]);
         s1 = add2(s1, p);
@@ -414,12 +458,15 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
       if (!in[i]) continue;
       Chunk xv, gv;
       chunk(i, xv, gv);
+      const float2 rx = factor(i);
 #pragma unroll
       for (int j = 0; j < kChunk / 2; ++j) {
-        const float2 xh = fma2(xv.p[j], r2, off);
+        const float2 xh = fma2(xv.p[j], rx, off);
         xv.p[j] = fma2(mul2(gv.p[j], w[i].p[j]), r2, fma2(xh, c1, c0));
       }
-      store_row_chunk<T, VEC>(static_cast<T*>(a.gx) + (int64_t)row * a.width, i, t, threads, a.width, xv);
+      T* const out = static_cast<T*>(a.gx) + (int64_t)row * a.width;
+      if (VEC) store_chunk(out + t * kChunk + i * threads * kChunk, xv);
+      else store_any_chunk(out, i, t, threads, a.width, xv);
     }
     fetch(row + a.stages * step);
     next_stage();
@@ -432,26 +479,27 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormArgs a)
   if (VEC) copy_wait<0>();  // nothing but empty groups is left
   if (!a.want_w && !a.want_b) return;
 
-  // the block's groups, added in order in shared memory (the ring is free now)
-  float* fold = reinterpret_cast<float*>(ring);
+  // the sums of the block's groups side by side in shared memory (the rings are done with), added in order
+  float* const fold = reinterpret_cast<float*>(ring);
+  __syncthreads();
+  auto put = [&](float* row, int i, const Chunk& v) {
+    if (VEC) {
+      if (in[i]) store_chunk(row + column<true>(i, 0, t, threads), v);
+    } else {
+      store_any_chunk(row, i, t, threads, a.width, v);
+    }
+  };
 #pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    if (!(pass ? a.want_b : a.want_w)) continue;
-    float* out = a.partial + ((int64_t)pass * gridDim.x + blockIdx.x) * a.width;
-    for (int y = 0; y < (int)blockDim.y; ++y) {
-      __syncthreads();
-      if (group == y)
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            const int c = column<VEC>(i, j, t, threads);
-            if (c < a.width) {
-              const float v = (y ? fold[c] : 0.f) + (pass ? db[SUMB ? i : 0][j] : dw[i][j]);
-              if (y + 1 == (int)blockDim.y) out[c] = v;
-              else fold[c] = v;
-            }
-          }
+  for (int i = 0; i < NV; ++i) {
+    put(fold + group * a.width, i, dw[i]);
+    if (SUMB) put(fold + (blockDim.y + group) * a.width, i, db[SUMB ? i : 0]);
+  }
+  __syncthreads();
+  for (int c = group * threads + t; c < a.width; c += all) {
+    for (int pass = 0; pass < (SUMB ? 2 : 1); ++pass) {
+      float s = 0.f;
+      for (int y = 0; y < (int)blockDim.y; ++y) s += fold[(pass * blockDim.y + y) * a.width + c];
+      a.partial[((int64_t)pass * gridDim.x + blockIdx.x) * a.width + c] = s;
     }
   }
 }
@@ -502,16 +550,24 @@ Shape shape_for(int width, int most, int warps_rows) {
   return {most, ceil_div(chunks, most * 32) * 32, 1};
 }
 
-// Forward: 16-bit rows wait in registers as they came, so a thread can hold eight chunks.
+// Forward: eight chunks of a 16-bit row a thread keep a block's warps, and the
+// time they wait for one another, few (8192 x 7168 bf16: 40 us, with four 45);
+// a checkpoint's eight do not fit the registers (4096 x 2816 from INT8: 16 us,
+// with four 11.5). Few rows want many threads each (1 x 7168: eight chunks
+// 3.8 us, four 3.0, two 2.5).
 Shape fwd_shape(const NormArgs& a, int type, bool vec) {
-  return shape_for(a.width, vec && !a.in_codes && type != RAWINT4_TYPE_F32 ? 8 : 4, kFwdWarps);
+  int most = vec && !a.in_codes && type != RAWINT4_TYPE_F32 ? 8 : 4;
+  if (a.rows <= kFewRows && a.width <= 2 * kChunk * 512) most = 2;
+  return shape_for(a.width, most, a.rows <= kFewRows ? 1 : kFwdWarps);
 }
 
-// Backward: 32 registers a thread for each of w, dw and db at four chunks; with
-// db the block takes two chunks a thread where the row's threads then still fit.
-Shape bwd_shape(int width, bool bias) {
-  Shape s = shape_for(width, bias && width <= 2 * kChunk * kBwdThreads ? 2 : 4, 1);
-  s.rows = kBwdThreads / s.threads;
+// Backward: two chunks a thread where the row's threads then fit a block.
+Shape bwd_shape(const NormArgs& a) {
+  const bool ckpt = a.in_codes != nullptr;
+  Shape s = shape_for(a.width, 2, 1);
+  if (s.threads > bwd_threads(2, a.want_b, ckpt)) s = shape_for(a.width, 4, 1);
+  s.rows = bwd_threads(s.nv, a.want_b, ckpt) / s.threads;
+  if (s.threads > 32 && s.rows > 15) s.rows = 15;  // named barriers
   return s;
 }
 
@@ -528,12 +584,13 @@ int stage_bytes(const Shape& s, int type, bool ckpt) {
 
 template <class T, int NV, bool VEC, bool CKPT, bool SUMB>
 cudaError_t launch_bwd(NormArgs a, int type, cudaStream_t st) {
-  const Shape s = bwd_shape(a.width, SUMB);
+  const Shape s = bwd_shape(a);
   const int stage = stage_bytes(s, type, CKPT);
   a.stages = VEC ? kBwdRing / stage : 1;
   if (a.stages > kBwdMaxStages) a.stages = kBwdMaxStages;
+  const int sums = (SUMB ? 2 : 1) * s.rows * a.width * (int)sizeof(float);
   int smem = VEC ? a.stages * stage : 0;
-  if (smem < a.width * (int)sizeof(float)) smem = a.width * (int)sizeof(float);
+  if (smem < sums) smem = sums;
   static std::atomic<unsigned long long> opted{0};
   int dev = 0;
   if (!device_flag_test(opted, &dev)) {
@@ -555,7 +612,7 @@ cudaError_t launch_fwd(const NormArgs& a, const Shape& s, cudaStream_t st) {
 template <class T, int NV>
 cudaError_t pick_fwd(const NormArgs& a, const Shape& s, bool vec, cudaStream_t st) {
   if (a.in_codes)
-    return vec ? launch_fwd<T, float, NV, true, true>(a, s, st) : launch_fwd<T, float, NV, false, true>(a, s, st);
+    return vec ? launch_fwd<T, __half, NV, true, true>(a, s, st) : launch_fwd<T, float, NV, false, true>(a, s, st);
   return vec ? launch_fwd<T, T, NV, true, false>(a, s, st) : launch_fwd<T, float, NV, false, false>(a, s, st);
 }
 
@@ -582,7 +639,7 @@ cudaError_t pick_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
 
 template <class T>
 cudaError_t run_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
-  const int nv = bwd_shape(a.width, a.want_b).nv;
+  const int nv = bwd_shape(a).nv;
   if (nv == 1) return pick_bwd<T, 1>(a, type, vec, st);
   if (nv == 2) return pick_bwd<T, 2>(a, type, vec, st);
   return pick_bwd<T, 4>(a, type, vec, st);
@@ -740,7 +797,7 @@ RAWINT4_API int rawint4_norm_bwd(const rawint4_norm_cfg* cfg, const void* x, int
   }
   if (sums) {
     R4_PROF("norm_fold", st);
-    if (launch_fold(a.partial, bwd_blocks(bwd_shape(a.width, a.want_b), a.rows), a.width, grad_weight, grad_bias, cfg->weight_type,
+    if (launch_fold(a.partial, bwd_blocks(bwd_shape(a), a.rows), a.width, grad_weight, grad_bias, cfg->weight_type,
                     accumulate, st) != cudaSuccess)
       return RAWINT4_CUDA_ERROR;
   }

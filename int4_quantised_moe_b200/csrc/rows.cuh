@@ -187,9 +187,11 @@ __device__ __forceinline__ uint2 ckpt_codes8(const Chunk& f, float inv, int fmt)
   if (fmt == RAWINT4_CKPT_E4M3) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(f.p[2 * h], both(inv)), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(f.p[2 * h + 1], both(inv)), __NV_SATFINITE, __NV_E4M3);
-      w[h] = lo | hi << 16;
+      const float2 a = mul2(f.p[2 * h], both(inv)), b = mul2(f.p[2 * h + 1], both(inv));
+      asm("{\n.reg .b16 lo, hi;\ncvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\ncvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+          "mov.b32 %0, {lo, hi};\n}"
+          : "=r"(w[h])
+          : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     }
   } else {
 #pragma unroll
@@ -266,33 +268,41 @@ __device__ __forceinline__ uint32_t ckpt_safe_byte(int fmt) {
   return (sizeof(T) == 2 && Elem<T>::kMax < 1e5f ? 127u + 7u : 127u + 119u) + (fmt == RAWINT4_CKPT_E4M3 ? 0u : 2u);
 }
 
+// The numbers that eight codes stand for, without their scale, in fp16 (exact;
+// INT8 through 1024 + (code + 128), which fp16 holds in its low bits).
+__device__ __forceinline__ RawChunk<__half> ckpt_numbers8(uint2 w, int fmt) {
+  RawChunk<__half> r;
+  if (fmt == RAWINT4_CKPT_E4M3) {
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(r.w[0]), "=r"(r.w[1])
+        : "r"(w.x));
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(r.w[2]), "=r"(r.w[3])
+        : "r"(w.y));
+  } else {
+    const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t v = __byte_perm(u[q / 2], 0x64006400u, (q & 1) ? 0x7372 : 0x7170);
+      const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), __half2half2(__ushort_as_half(0x6480)));  // 1152
+      r.w[q] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+    if (__vcmpeq4(w.x, 0x80808080u) | __vcmpeq4(w.y, 0x80808080u)) {  // rare: NaN codes
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j)
+        if ((u[j / 4] >> (8 * (j % 4)) & 0xFFu) == 0u) r.w[j / 2] |= 0x7FFFu << (16 * (j & 1));
+    }
+  }
+  return r;
+}
+
 // Eight values of a checkpoint, saturated for type T.
 template <class T>
 __device__ __forceinline__ Chunk ckpt_decode8(uint2 w, uint32_t byte, int fmt) {
+  Chunk f = widen<__half>(ckpt_numbers8(w, fmt));
   const float2 scale = both(ckpt_scale(byte));
-  Chunk f;
-  if (fmt == RAWINT4_CKPT_E4M3) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t two = ((q < 2 ? w.x : w.y) >> (16 * (q & 1))) & 0xFFFFu;
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-      f.p[q] = mul2(__half22float2(__half2(h)), scale);
-    }
-  } else {
-    const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};  // code + 128 in the low bits of 2^23
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t sel = 0x7440 + 2 * (q & 1);
-      const float2 v = make_float2(__uint_as_float(__byte_perm(u[q / 2], 0x4B000000u, sel)),
-                                   __uint_as_float(__byte_perm(u[q / 2], 0x4B000000u, sel + 1)));
-      f.p[q] = mul2(add2(v, both(-8388736.f)), scale);
-    }
-    if (__vcmpeq4(w.x, 0x80808080u) | __vcmpeq4(w.y, 0x80808080u)) {
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j)
-        if ((u[j / 4] >> (8 * (j % 4)) & 0xFFu) == 0u) f[j] = __uint_as_float(0x7FC00000u);
-    }
-  }
+  for (int q = 0; q < 4; ++q) f.p[q] = mul2(f.p[q], scale);
   if (byte > ckpt_safe_byte<T>(fmt)) {
 #pragma unroll
     for (int j = 0; j < kChunk; ++j) f[j] = ckpt_saturate(f[j], Elem<T>::kMax);
