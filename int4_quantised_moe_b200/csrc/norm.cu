@@ -508,6 +508,7 @@ __global__ void __launch_bounds__(bwd_threads(NV, SUMB, CKPT)) norm_bwd_kernel(c
 // A warp reads 32 neighbouring columns of every 16th row; the 16 sums are
 // added in order.
 constexpr int kFoldWarps = 16;
+constexpr int kFoldRows = (kBwdBlocks + kFoldWarps - 1) / kFoldWarps;
 __global__ void __launch_bounds__(32 * kFoldWarps) norm_fold_kernel(const float* __restrict__ partial, int blocks,
                                                                     int width, void* gw, void* gb, int type,
                                                                     int accumulate) {
@@ -518,10 +519,15 @@ __global__ void __launch_bounds__(32 * kFoldWarps) norm_fold_kernel(const float*
   void* out = blockIdx.y ? gb : gw;
   if (!out) return;
   const float* p = partial + (int64_t)blockIdx.y * blocks * width + c;
+  float v[kFoldRows];  // all on their way at once
+#pragma unroll
+  for (int i = 0; i < kFoldRows; ++i) {
+    const int b = warp + i * kFoldWarps;
+    v[i] = c < width && b < blocks ? p[(int64_t)b * width] : 0.f;
+  }
   float s = 0.f;
-  if (c < width)
-#pragma unroll 4
-    for (int b = warp; b < blocks; b += kFoldWarps) s += p[(int64_t)b * width];
+#pragma unroll
+  for (int i = 0; i < kFoldRows; ++i) s += v[i];
   sums[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= width) return;
