@@ -151,6 +151,12 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 
+try:
+    from . import _fastcall as _fast  # csrc/fastcall.cpp
+except ImportError as e:
+    raise ImportError(f"the _fastcall extension beside {LIB_PATH} is missing or does not load ({e}): build it with "
+                      "`python -m int4_quantised_moe_b200.build`") from e
+
 
 def library() -> ctypes.CDLL:
     return _lib
@@ -481,6 +487,10 @@ def router_bwd(scores: torch.Tensor, ids: torch.Tensor, grad_route: torch.Tensor
 # runs on; tensors passed to a call on another stream are recorded there, so
 # they may be dropped at once. Using a result on a third stream is ordered by
 # the caller, as with any torch operation.
+#
+# The ordinary call (right arguments, current device and stream) is made by the
+# _fastcall extension; it answers None to every other one, which is then checked
+# and made here.
 
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -560,6 +570,10 @@ def router_select(scores: torch.Tensor, cfg: SelectCfg, bias: Optional[torch.Ten
     fp16): sigmoid or softmax, a balance bias fp32 [E] that ranks only, groups, top-k, optionally
     renormalised, times cfg.scale. `counts` int32 [E] (optional, overwritten) receives the slots routed
     to each expert."""
+    if stream is None:
+        r = _fast.router_select(scores, cfg, bias, counts)
+        if r is not None:
+            return r if type(r) is tuple else _check(r, "rawint4_moe_router_select")
     E = cfg.experts
     pitch = _rows(scores, "scores", E)
     dev = scores.device
@@ -584,6 +598,10 @@ def router_select(scores: torch.Tensor, cfg: SelectCfg, bias: Optional[torch.Ten
 def router_select_bwd(scores: torch.Tensor, cfg: SelectCfg, ids: torch.Tensor, grad_route: torch.Tensor,
                       stream=None) -> torch.Tensor:
     """dL/dscores [Q, E] in the scores' type from the layer's grad_route fp32 [Q, k]."""
+    if stream is None:
+        r = _fast.router_select_bwd(scores, cfg, ids, grad_route)
+        if r is not None:
+            return _check(r, "rawint4_moe_router_select_bwd") if type(r) is int else r
     pitch = _rows(scores, "scores", cfg.experts)
     dev = scores.device
     q = scores.shape[0]
@@ -634,6 +652,10 @@ def _empty_ckpt8(x: torch.Tensor, fmt: str) -> Ckpt8:
 def ckpt8_save(x: torch.Tensor, format: str = "e4m3", stream=None) -> Ckpt8:
     """x [rows, width] (fp32, bf16 or fp16) in 8 bits; see include/rawint4_moe.h for the format."""
     fmt = _choice(CKPT_FORMATS, format, "format")
+    if stream is None:
+        r = _fast.ckpt8_save(x, fmt)
+        if r is not None:
+            return Ckpt8(r[0], r[1], format) if type(r) is tuple else _check(r, "rawint4_ckpt8_save")
     pitch = _rows(x, "x")
     ctx = _elsewhere(x.device, stream, x)
     if ctx is not None:
@@ -648,6 +670,10 @@ def ckpt8_save(x: torch.Tensor, format: str = "e4m3", stream=None) -> Ckpt8:
 
 def ckpt8_load(ckpt: Ckpt8, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """The rows of a checkpoint, [rows, width] in `dtype`."""
+    if stream is None and ckpt.format in CKPT_FORMATS:
+        r = _fast.ckpt8_load(ckpt.codes, ckpt.scales, CKPT_FORMATS[ckpt.format], dtype)
+        if r is not None:
+            return _check(r, "rawint4_ckpt8_load") if type(r) is int else r
     fmt = ckpt.check("ckpt")
     typ = _choice(TYPES, dtype, "dtype")
     codes = ckpt.codes
@@ -660,6 +686,13 @@ def ckpt8_load(ckpt: Ckpt8, dtype: torch.dtype = torch.bfloat16, stream=None) ->
     _check(_lib.rawint4_ckpt8_load(fmt, codes.data_ptr(), ckpt.scales.data_ptr(), rows, width, typ, out.data_ptr(),
                                    _here(codes.device)), "rawint4_ckpt8_load")
     return out
+
+
+def _fast_input(x) -> tuple:
+    """(x, codes, scales, format) for the extension."""
+    if isinstance(x, Ckpt8):
+        return None, x.codes, x.scales, CKPT_FORMATS.get(x.format, -1)
+    return x, None, None, 0
 
 
 def _norm_input(x, name: str):
@@ -683,6 +716,13 @@ def norm_fwd(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tens
     """Layer or RMS norm of the rows of x, a tensor [rows, width] or a Ckpt8 (then `dtype` is the
     result's type, bf16 by default). Returns (y, mean, rstd, ckpt): mean is None for kind "rms", ckpt is
     x in 8 bits when `save` names a format, else None."""
+    if stream is None and kind in NORM_KINDS and (save is None or save in CKPT_FORMATS):
+        r = _fast.norm_fwd(*_fast_input(x), weight, bias, NORM_KINDS[kind], eps, dtype,
+                           -1 if save is None else CKPT_FORMATS[save])
+        if r is not None:
+            if type(r) is int:
+                _check(r, "rawint4_norm_fwd")
+            return r[0], r[1], r[2], None if save is None else Ckpt8(r[3], r[4], save)
     rows, width, dev, ptr, pitch, ck = _norm_input(x, "x")
     k = _choice(NORM_KINDS, kind, "kind")
     if ck is None:
@@ -727,6 +767,11 @@ def norm_bwd(grad_y: torch.Tensor, x, rstd: torch.Tensor, weight: Optional[torch
     """Backward of norm_fwd from its input x (a tensor, or the Ckpt8 kept in its place) and statistics.
     Returns (grad_x, grad_weight, grad_bias) in the types of grad_y and of the weight; grad_weight is None
     without a weight, grad_bias unless it is asked for. Buffers may be given; accumulate=True adds to them."""
+    if stream is None and kind in NORM_KINDS:
+        r = _fast.norm_bwd(*_fast_input(x), grad_y, rstd, weight, mean, NORM_KINDS[kind], bias_grad, grad_weight,
+                           grad_bias, accumulate)
+        if r is not None:
+            return r if type(r) is tuple else _check(r, "rawint4_norm_bwd")
     rows, width, dev, ptr, pitch, ck = _norm_input(x, "x")
     k = _choice(NORM_KINDS, kind, "kind")
     gpitch = _rows(grad_y, "grad_y", width, dev, None if ck is not None else x.dtype)

@@ -15,6 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librawint4_moe.so")
+FASTCALL = os.path.join(HERE, "_fastcall.so")  # CPython extension over LIB: the quick way in for torch tensors
+FASTCALL_SOURCE = os.path.join(CSRC, "fastcall.cpp")
 SOURCES = ["api.cu", "gemm_pair.cu", "gemm_tm.cu", "gemm_pair_narrow.cu", "gemm_tm_narrow.cu", "skinny.cu", "route.cu",
            "aux.cu", "prof.cu", "noalloc.cu", "router.cu", "select.cu", "select_f32.cu", "select_bf16.cu",
            "select_f16.cu", "norm.cu", "ckpt8.cu"]
@@ -33,11 +35,32 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(FASTCALL):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "rawint4_moe.h")]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(FASTCALL))
+    deps = [FASTCALL_SOURCE] + [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "rawint4_moe.h")]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+
+
+def _build_fastcall(verbose: bool) -> None:
+    """Compile fastcall.cpp against this Python and torch, linked to LIB beside it."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = FASTCALL + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-isystem{p}" for p in include], FASTCALL_SOURCE, "-o", tmp, f"-L{HERE}", "-l:librawint4_moe.so",
+           "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+           "-ltorch_cuda", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, FASTCALL)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -62,6 +85,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _build_fastcall(verbose)
     return LIB
 
 
