@@ -33,6 +33,7 @@ template <class T, int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt8_save_vec(const T* __restrict__ x, int64_t ldx, int64_t n, int width,
                                                            uint32_t cpr, uint8_t* __restrict__ codes,
                                                            uint8_t* __restrict__ scales, int groups) {
+  begin_after_previous();
   const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
   RawChunk<T> r[kUnroll];
 #pragma unroll
@@ -64,6 +65,7 @@ template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt8_save_any(const T* __restrict__ x, int64_t ldx, int64_t n, int width,
                                                            int fmt, uint8_t* __restrict__ codes,
                                                            uint8_t* __restrict__ scales, uint32_t groups) {
+  begin_after_previous();
   const int lane = threadIdx.x & 31;
   const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
   float f[kUnroll];
@@ -89,6 +91,7 @@ template <class T, int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt8_load_vec(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales, int64_t n, int width,
                                                            uint32_t cpr, int groups, T* __restrict__ out) {
+  begin_after_previous();
   const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
   uint2 w[kUnroll];
   uint32_t byte[kUnroll];
@@ -120,6 +123,7 @@ template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt8_load_any(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales, int64_t n, int width,
                                                            uint32_t groups, int fmt, T* __restrict__ out) {
+  begin_after_previous();
   const int lane = threadIdx.x & 31;
   const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnroll;
   uint32_t code[kUnroll], byte[kUnroll];
@@ -150,8 +154,7 @@ cudaError_t slices(int64_t rows, int64_t per_row, int64_t per_block, F run) {
   const int64_t step = ((int64_t)1 << 31) / per_row;
   for (int64_t r = 0; r < rows; r += step) {
     const int64_t n = (rows - r < step ? rows - r : step) * per_row;
-    run(r, n, (unsigned)((n + per_block - 1) / per_block));
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = run(r, n, (unsigned)((n + per_block - 1) / per_block));
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
@@ -172,11 +175,11 @@ cudaError_t save(int type, const void* x, int64_t ldx, int64_t rows, int width, 
   const T* p = static_cast<const T*>(x);
   if (width % kChunk == 0 && rows_aligned(x, ldx, type) && reinterpret_cast<uintptr_t>(codes) % 8 == 0)
     return slices(rows, groups * kGroupChunks, kVecUnits, [&](int64_t r, int64_t n, unsigned blocks) {
-      ckpt8_save_vec<T, FMT><<<blocks, kThreads, 0, st>>>(p + r * ldx, ldx, n, width, chunks_per_row(width, ldx),
+      return launch_early(ckpt8_save_vec<T, FMT>, blocks, kThreads, 0, st, p + r * ldx, ldx, n, width, chunks_per_row(width, ldx),
                                                           codes + r * width, scales + r * groups, groups);
     });
   return slices(rows, groups, kAnyUnits, [&](int64_t r, int64_t n, unsigned blocks) {
-    ckpt8_save_any<T><<<blocks, kThreads, 0, st>>>(p + r * ldx, ldx, n, width, FMT, codes + r * width,
+    return launch_early(ckpt8_save_any<T>, blocks, kThreads, 0, st, p + r * ldx, ldx, n, width, FMT, codes + r * width,
                                                    scales + r * groups, groups);
   });
 }
@@ -188,11 +191,11 @@ cudaError_t load(int type, const uint8_t* codes, const uint8_t* scales, int64_t 
   T* p = static_cast<T*>(out);
   if (width % kChunk == 0 && rows_aligned(out, width, type) && reinterpret_cast<uintptr_t>(codes) % 8 == 0)
     return slices(rows, groups * kGroupChunks, kVecUnits, [&](int64_t r, int64_t n, unsigned blocks) {
-      ckpt8_load_vec<T, FMT><<<blocks, kThreads, 0, st>>>(codes + r * width, scales + r * groups, n, width,
+      return launch_early(ckpt8_load_vec<T, FMT>, blocks, kThreads, 0, st, codes + r * width, scales + r * groups, n, width,
                                                           chunks_per_row(width, width), groups, p + r * width);
     });
   return slices(rows, groups, kAnyUnits, [&](int64_t r, int64_t n, unsigned blocks) {
-    ckpt8_load_any<T><<<blocks, kThreads, 0, st>>>(codes + r * width, scales + r * groups, n, width, groups, FMT,
+    return launch_early(ckpt8_load_any<T>, blocks, kThreads, 0, st, codes + r * width, scales + r * groups, n, width, groups, FMT,
                                                    p + r * width);
   });
 }

@@ -15,9 +15,8 @@
 // their own chunks of the coming rows into shared memory (cp.async, a ring of
 // a few rows), so no barrier guards the ring and several rows are in flight
 // while one is computed. dw and db of a thread's columns stay in its
-// registers; each block writes one partial row of sums, and a second kernel,
-// launched early (its start overlaps the first one's tail), adds the partials
-// in block order, so the result does not depend on timing.
+// registers; each block writes one partial row of sums, and a second kernel
+// adds the partials in block order, so the result does not depend on timing.
 #include "prof.cuh"
 #include "rows.cuh"
 
@@ -186,6 +185,7 @@ template <class T, class R, int NV, bool VEC, bool CKPT>
 __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormArgs a) {
   __shared__ float buf[2][16];
   constexpr bool kScaled = VEC && CKPT;
+  begin_after_previous();
   const int t = threadIdx.x, threads = blockDim.x;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps leave; a block-wide row never does
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(bwd_threads(NV, SUMB, CKPT)) norm_bwd_kernel(c
   const int warp0 = group * (threads >> 5);  // a group's part of buf
   const int step = gridDim.x * blockDim.y;
   const float inv_n = 1.0f / (float)a.width;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  begin_after_previous();
 
   // slots of this thread: [stage][chunk][thread], x behind dy
   constexpr int kG = (int)sizeof(RawChunk<T>);
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(32 * kFoldWarps) norm_fold_kernel(const float*
                                                                     int width, void* gw, void* gb, int type,
                                                                     int accumulate) {
   __shared__ float sums[kFoldWarps][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial rows are complete and visible
+  begin_after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   void* out = blockIdx.y ? gb : gw;
@@ -605,14 +605,12 @@ cudaError_t launch_bwd(NormArgs a, int type, cudaStream_t st) {
     if (err != cudaSuccess) return err;
     device_flag_set(opted, dev);
   }
-  norm_bwd_kernel<T, NV, VEC, CKPT, SUMB><<<bwd_blocks(s, a.rows), dim3(s.threads, s.rows), smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(norm_bwd_kernel<T, NV, VEC, CKPT, SUMB>, bwd_blocks(s, a.rows), dim3(s.threads, s.rows), smem, st, a);
 }
 
 template <class T, class R, int NV, bool VEC, bool CKPT>
 cudaError_t launch_fwd(const NormArgs& a, const Shape& s, cudaStream_t st) {
-  norm_fwd_kernel<T, R, NV, VEC, CKPT><<<ceil_div(a.rows, s.rows), dim3(s.threads, s.rows), 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(norm_fwd_kernel<T, R, NV, VEC, CKPT>, ceil_div(a.rows, s.rows), dim3(s.threads, s.rows), 0, st, a);
 }
 
 template <class T, int NV>
@@ -649,21 +647,6 @@ cudaError_t run_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
   if (nv == 1) return pick_bwd<T, 1>(a, type, vec, st);
   if (nv == 2) return pick_bwd<T, 2>(a, type, vec, st);
   return pick_bwd<T, 4>(a, type, vec, st);
-}
-
-// The second kernel may start while the first one ends; it waits for it itself.
-cudaError_t launch_fold(const float* partial, int blocks, int width, void* gw, void* gb, int type, int accumulate,
-                        cudaStream_t st) {
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ceil_div(width, 32), 2);
-  cfg.blockDim = dim3(32 * kFoldWarps);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_fold_kernel, partial, blocks, width, gw, gb, type, accumulate);
 }
 
 bool cfg_ok(const rawint4_norm_cfg* c) {
@@ -803,8 +786,9 @@ RAWINT4_API int rawint4_norm_bwd(const rawint4_norm_cfg* cfg, const void* x, int
   }
   if (sums) {
     R4_PROF("norm_fold", st);
-    if (launch_fold(a.partial, bwd_blocks(bwd_shape(a), a.rows), a.width, grad_weight, grad_bias, cfg->weight_type,
-                    accumulate, st) != cudaSuccess)
+    if (launch_early(norm_fold_kernel, dim3(ceil_div(a.width, 32), 2), 32 * kFoldWarps, 0, st, a.partial,
+                     bwd_blocks(bwd_shape(a), a.rows), a.width, grad_weight, grad_bias, cfg->weight_type,
+                     accumulate) != cudaSuccess)
       return RAWINT4_CUDA_ERROR;
   }
   return RAWINT4_OK;

@@ -310,6 +310,16 @@ __device__ __forceinline__ Chunk ckpt_decode8(uint2 w, uint32_t byte, int fmt) {
   return f;
 }
 
+// Kernels of this kind follow one another in a stream within microseconds, so
+// each may be launched while the one before it drains: begin_after_previous()
+// stands before a kernel's first access to memory and returns when everything
+// before it in the stream is complete and visible; it also lets the next
+// kernel's blocks take the places that this one's last blocks leave.
+__device__ __forceinline__ void begin_after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ float row_warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -317,6 +327,22 @@ __device__ __forceinline__ float row_warp_sum(float v) {
 }
 
 // ------------------------------------------------------------- host side
+// Launch of a kernel that starts with begin_after_previous().
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 constexpr int64_t kMaxPitch = (int64_t)1 << 28;  // elements of a row pitch
 
 inline size_t type_size(int type) { return type == RAWINT4_TYPE_F32 ? 4 : 2; }

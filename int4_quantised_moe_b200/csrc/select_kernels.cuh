@@ -335,6 +335,7 @@ __device__ __forceinline__ bool close_groups(const SelectArgs& a, const float (&
 
 template <class T, int NI, bool VEC, bool BIAS>
 __global__ void __launch_bounds__(32 * kWarps, NI <= 4 ? 2 : 1) select_kernel(const SelectArgs a) {
+  begin_after_previous();
   constexpr int NP = 4 * NI;
   constexpr bool kWhole = sizeof(T) == 2 && !BIAS;  // 16-bit scores ranked as they are: all their bits, no rounding
   constexpr int kIndexBits = NI == 1 ? 7 : NI == 2 ? 8 : NI <= 4 ? 9 : 10;
@@ -543,6 +544,7 @@ __global__ void __launch_bounds__(32 * kWarps, NI <= 4 ? 2 : 1) select_kernel(co
 // Rows of more than 1024 experts: the keys lie in shared memory, in double.
 template <class T>
 __global__ void __launch_bounds__(32 * kWarps) select_wide_kernel(const SelectArgs a) {
+  begin_after_previous();
   extern __shared__ uint64_t keys[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int t = blockIdx.x * warps + warp; t < a.Q; t += gridDim.x * warps) {
@@ -609,6 +611,7 @@ __device__ __forceinline__ Chunk score_chunk(const T* z, int e, int E) {
 
 template <class T, int LANES, int NI, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads) select_bwd_kernel(const SelectArgs a) {
+  begin_after_previous();
   const int lane = threadIdx.x % LANES;
   const int t = (blockIdx.x * kBwdThreads + threadIdx.x) / LANES;
   const bool live = t < a.Q;
@@ -747,8 +750,7 @@ cudaError_t start(K kernel, std::atomic<unsigned long long>& opted, const Select
     if (err != cudaSuccess) return err;
     device_flag_set(opted, dev);
   }
-  kernel<<<s.blocks, 32 * s.warps, s.smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(kernel, s.blocks, 32 * s.warps, s.smem, st, a);
 }
 
 template <class T, int NI, bool VEC, bool BIAS>
@@ -780,26 +782,24 @@ cudaError_t select_type(const SelectArgs& a, int sms, cudaStream_t st) {
 constexpr int kManyTokens = 32768;
 
 template <class T, int LANES, int NI>
-void launch_bwd(const SelectArgs& a, cudaStream_t st) {
+cudaError_t launch_bwd(const SelectArgs& a, cudaStream_t st) {
   const int tokens = kBwdThreads / LANES, blocks = (a.Q + tokens - 1) / tokens;
   const int type = sizeof(T) == 4 ? RAWINT4_TYPE_F32 : RAWINT4_TYPE_BF16;  // a size
-  if (a.E % kChunk == 0 && rows_aligned(a.scores, a.ld, type) && rows_aligned(a.grad, a.E, type))
-    select_bwd_kernel<T, LANES, NI, true><<<blocks, kBwdThreads, 0, st>>>(a);
-  else
-    select_bwd_kernel<T, LANES, NI, false><<<blocks, kBwdThreads, 0, st>>>(a);
+  const bool vec = a.E % kChunk == 0 && rows_aligned(a.scores, a.ld, type) && rows_aligned(a.grad, a.E, type);
+  return launch_early(vec ? select_bwd_kernel<T, LANES, NI, true> : select_bwd_kernel<T, LANES, NI, false>, blocks,
+                      kBwdThreads, 0, st, a);
 }
 
 template <class T>
 cudaError_t select_bwd_type(const SelectArgs& a, cudaStream_t st) {
   const bool few = a.k <= 8 && a.Q >= kManyTokens, all = !a.sigmoid && !a.renorm;
-  if (!all) few ? launch_bwd<T, 8, 0>(a, st) : launch_bwd<T, 32, 0>(a, st);
-  else if (few && a.E <= 128) launch_bwd<T, 8, 2>(a, st);
-  else if (few && a.E <= 256) launch_bwd<T, 8, 4>(a, st);
-  else if (a.E <= 256) launch_bwd<T, 32, 1>(a, st);
-  else if (a.E <= 512) launch_bwd<T, 32, 2>(a, st);
-  else if (a.E <= 1024) launch_bwd<T, 32, 4>(a, st);
-  else launch_bwd<T, 32, 0>(a, st);
-  return cudaGetLastError();
+  if (!all) return few ? launch_bwd<T, 8, 0>(a, st) : launch_bwd<T, 32, 0>(a, st);
+  if (few && a.E <= 128) return launch_bwd<T, 8, 2>(a, st);
+  if (few && a.E <= 256) return launch_bwd<T, 8, 4>(a, st);
+  if (a.E <= 256) return launch_bwd<T, 32, 1>(a, st);
+  if (a.E <= 512) return launch_bwd<T, 32, 2>(a, st);
+  if (a.E <= 1024) return launch_bwd<T, 32, 4>(a, st);
+  return launch_bwd<T, 32, 0>(a, st);
 }
 
 }  // namespace

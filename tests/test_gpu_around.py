@@ -523,11 +523,12 @@ def test_norm_past_32_bit_offsets(B):
 # ----------------------------------------------------- streams, graphs, overlap
 
 def _pass(B, z, cfg, bias, gr, x, w, gy):
-    ids, wt = B.router_select(z, cfg, bias)
+    counts = torch.empty(128, dtype=torch.int32, device="cuda")
+    ids, wt = B.router_select(z, cfg, bias, counts=counts)
     gz = B.router_select_bwd(z, cfg, ids, gr)
     y, mean, rstd, ck = B.norm_fwd(x, w, save="int8")
     dx, dw, _ = B.norm_bwd(gy, ck, rstd, w)
-    return ids, wt, gz, y, ck.codes, dx, dw, B.ckpt8_load(ck)
+    return ids, wt, gz, y, ck.codes, dx, dw, B.ckpt8_load(ck), counts
 
 
 def _operands(seed):
