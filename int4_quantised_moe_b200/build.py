@@ -19,8 +19,9 @@ FASTCALL = os.path.join(HERE, "_fastcall.so")  # CPython extension over LIB: the
 FASTCALL_SOURCE = os.path.join(CSRC, "fastcall.cpp")
 SOURCES = ["api.cu", "gemm_pair.cu", "gemm_tm.cu", "gemm_pair_narrow.cu", "gemm_tm_narrow.cu", "skinny.cu", "route.cu",
            "aux.cu", "prof.cu", "noalloc.cu", "router.cu", "select.cu", "select_f32.cu", "select_bf16.cu",
-           "select_f16.cu", "norm.cu", "ckpt8.cu"]
-HEADERS = ["common.cuh", "gemm.cuh", "skinny.cuh", "route.cuh", "aux.cuh", "prof.cuh", "router.cuh", "rows.cuh", "select.cuh", "select_kernels.cuh"]
+           "select_f16.cu", "norm.cu", "norm_fwd.cu", "norm_bwd_f32.cu", "norm_bwd_bf16.cu", "norm_bwd_f16.cu", "ckpt8.cu"]
+HEADERS = ["common.cuh", "gemm.cuh", "skinny.cuh", "route.cuh", "aux.cuh", "prof.cuh", "router.cuh", "rows.cuh", "select.cuh",
+           "select_kernels.cuh", "norm.cuh", "norm_kernels.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -1,0 +1,88 @@
+#pragma once
+#include "rows.cuh"
+
+namespace r4 {
+
+constexpr int kMaxWidth = 16384;
+constexpr int kFewRows = 296;        // two rows an SM
+constexpr int kFwdWarps = 8;         // rows of a forward block when a row lies in one warp
+// Threads of a backward block at most, so that w, dw and db (8 registers a
+// chunk each) and a checkpoint's numbers (4) fit.
+__host__ __device__ constexpr int bwd_threads(int nv, bool bias, bool ckpt) {
+  return nv == 4 ? 512 : nv == 2 && bias ? (ckpt ? 576 : 640) : 896;
+}
+constexpr int kBwdBlocks = 148;      // blocks of the backward at most, one an SM: rows of partial sums
+constexpr int kBwdMaxStages = 4;     // rows in a thread group's ring
+constexpr int kBwdRing = 200 * 1024; // bytes of shared memory for the rings
+
+struct NormArgs {
+  const void* x;            // elements of type T, or
+  const uint8_t* in_codes;  // an 8-bit checkpoint
+  const uint8_t* in_scales;
+  int64_t ldx;
+  int in_fmt;
+  int rows, width, groups;
+  int layer;                // subtract the mean
+  int w_type;
+  float eps;
+  const void *weight, *bias;
+  void* y;
+  float *mean, *rstd;
+  uint8_t *codes, *scales;  // checkpoint to write (null: none)
+  int fmt;
+  // backward
+  const void* gy;
+  int64_t ldg;
+  const float *mean_in, *rstd_in;
+  void* gx;
+  float* partial;           // [2][blocks][width]: dw, db
+  int want_w, want_b;
+  int stages;
+};
+
+__device__ __forceinline__ float load_as(const void* p, int type, int64_t i) {
+  if (type == RAWINT4_TYPE_F32) return static_cast<const float*>(p)[i];
+  if (type == RAWINT4_TYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+struct Shape {
+  int nv, threads, rows;  // chunks a thread, threads a row, rows (row groups) a block
+};
+
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The smallest of `most`, most / 2, ... chunks a thread that a row of one warp
+// needs, else `most` and as many warps as that takes.
+inline Shape shape_for(int width, int most, int warps_rows) {
+  const int chunks = ceil_div(width, kChunk);
+  for (int nv = 1; nv <= most && nv <= 4; nv *= 2)
+    if (chunks <= 32 * nv) return {nv, 32, warps_rows};
+  return {most, ceil_div(chunks, most * 32) * 32, 1};
+}
+
+// Backward: four chunks a thread, with db two where the row's threads then fit
+// a block (8192 x 7168 bf16 RMS: 62 us, with two 78; 4096 x 2816 from INT8 with
+// db: 37 us, with two 27).
+inline Shape bwd_shape(const NormArgs& a) {
+  const bool ckpt = a.in_codes != nullptr;
+  Shape s = shape_for(a.width, a.want_b ? 2 : 4, 1);
+  if (s.threads > bwd_threads(2, a.want_b, ckpt)) s = shape_for(a.width, 4, 1);
+  s.rows = bwd_threads(s.nv, a.want_b, ckpt) / s.threads;
+  if (s.threads > 32 && s.rows > 15) s.rows = 15;  // named barriers
+  return s;
+}
+
+inline int bwd_blocks(const Shape& s, int rows) {
+  const int need = ceil_div(rows, s.rows);
+  return need < kBwdBlocks ? need : kBwdBlocks;
+}
+
+// The kernels for one element type (norm_fwd.cu, norm_bwd_f32.cu, norm_bwd_bf16.cu, norm_bwd_f16.cu);
+// `vec`: every row, weight and bias may move with vector accesses. a.rows > 0.
+template <class T>
+cudaError_t run_norm_fwd(const NormArgs& a, int type, bool vec, cudaStream_t st);
+template <class T>
+cudaError_t run_norm_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st);
+
+}  // namespace r4
