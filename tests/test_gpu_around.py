@@ -132,6 +132,57 @@ def test_select_and_gradient(B, case):
         assert not f64(grad)[mask].any()
 
 
+MANY = [
+    # E, k, score, dtype, bias, renorm, pad, Q
+    (128, 8, "softmax", "bf16", False, False, 0, 32768),
+    (128, 8, "sigmoid", "fp32", True, True, 0, 32769),
+    (128, 8, "softmax", "fp32", True, False, 8, 32770),
+    (64, 8, "sigmoid", "fp16", False, True, 0, 40003),
+    (60, 6, "softmax", "fp32", False, True, 3, 32771),
+    (8, 8, "sigmoid", "bf16", True, True, 0, 32768),
+    (5, 3, "softmax", "fp16", True, True, 1, 33000),
+    (1, 1, "sigmoid", "bf16", False, False, 0, 32768),
+    (100, 1, "softmax", "bf16", False, True, 0, 32768),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=[f"{c[0]}k{c[1]}-{c[2]}-{c[3]}" for c in MANY])
+def test_select_many_tokens(B, case):
+    """Batches of 32768 tokens and more take their own kernels: every token's selection is that of the
+    same token in a batch of 4096, every 97th is the oracle's; weights and gradients agree as two fp32
+    results of the same formulas do. Ties, masked experts, NaN and whole rows without a score included."""
+    E, k, score, dtype, bias, renorm, pad, Q = case
+    g = torch.Generator().manual_seed(E * 10 + k)
+    z = torch.randn((Q, E), generator=g) * 1.5
+    z[::5] = z[::5].round()  # ties
+    z[torch.rand((Q, E), generator=g) < 0.02] = -np.inf
+    z[3::211] = -np.inf
+    z[7::301, 0] = float("nan")
+    if E > 16:
+        z[11::103, 16:] = -np.inf  # all that is left lies in one lane
+        z[11::103, :16] = 9.0 + 1e-6 * torch.rand((len(range(11, Q, 103)), 16), generator=g)
+    z = z.to(DTYPES[dtype])
+    b = torch.randn(E, generator=g) * 0.1 if bias else None
+    gr = torch.randn((Q, k), generator=g)
+    zc, bc, gc = pitched(z, pad), None if b is None else b.cuda(), gr.cuda()
+    cfg = B.make_select_cfg(E, k, score=score, renormalise=renorm, scale=1.5)
+    counts = torch.empty(E, dtype=torch.int32, device="cuda")
+    ids, w = B.router_select(zc, cfg, bc, counts=counts)
+    grad = B.router_select_bwd(zc, cfg, ids, gc)
+    for lo in range(0, Q, 4096):
+        ids2, w2 = B.router_select(zc[lo:lo + 4096], cfg, bc)
+        assert torch.equal(ids[lo:lo + 4096], ids2)
+        torch.testing.assert_close(w[lo:lo + 4096], w2, rtol=64 * U, atol=0)
+        grad2 = B.router_select_bwd(zc[lo:lo + 4096], cfg, ids2, gc[lo:lo + 4096])
+        step = torch.finfo(z.dtype).eps  # two roundings of nearly the same value may differ by a step
+        torch.testing.assert_close(grad[lo:lo + 4096], grad2, rtol=2 * step, atol=64 * U * 8)
+    assert torch.equal(counts.cpu(), torch.bincount(ids.reshape(-1), minlength=E).int().cpu())
+    pick = sorted(set(range(0, Q, 97)) | set(range(11, Q, 1030)) | {Q - 1})
+    want, ow = oselect.forward(f64(z[pick]), k, score, None if b is None else f64(b), 1, 1, 1, renorm, 1.5)
+    assert np.array_equal(ids.cpu().numpy()[pick], want)
+    close(w[pick], ow, share_tolerance(z[pick], k) * ow, "weights")
+
+
 def test_select_gradient_against_differences(B):
     """Weights of the device at s + d and s - d against the device's gradient. d = 2^-6 is exact; the
     third derivative is at most 1 in magnitude times the scale and sum of |g|: d^2 / 6 of it; the
