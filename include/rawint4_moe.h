@@ -351,7 +351,7 @@ enum { RAWINT4_TYPE_F32 = 0, RAWINT4_TYPE_BF16 = 1, RAWINT4_TYPE_F16 = 2 }; /* e
  * bias of -inf or NaN ranks the expert last as well and leaves its weight.
  * Limits: experts <= 4096, top_k <= 32, groups <= 32, experts % groups == 0,
  * 1 <= groups_kept <= groups, group_top 1 or 2 (at most experts / groups),
- * top_k <= groups_kept * experts / groups, scale finite. */
+ * top_k <= groups_kept * experts / groups, scale finite, at most 2^30 tokens. */
 enum { RAWINT4_SCORE_SOFTMAX = 0, RAWINT4_SCORE_SIGMOID = 1 };
 typedef struct rawint4_moe_select_cfg {
   int32_t experts, top_k;

@@ -580,11 +580,12 @@ __global__ void __launch_bounds__(32 * kWarps, NI <= 4 ? 2 : 1) select_kernel(co
 }
 
 // ------------------------------------------------- many tokens, few experts
-// Four tokens a warp, eight lanes each: what a token costs beside its scores
-// (rounds, weights, stores) is shared by four. At most 128 experts and eight
-// slots, no groups. Lane l of a token holds experts 64 i + 8 l + j, i < 2,
-// j < 8, sorts their numbers and keeps the best eight in order, so a round is
-// three exchanges and a shift.
+// 16-bit scores ranked as they are, at most 128 experts, eight slots, no
+// groups: four tokens a warp, eight lanes each, so what a token costs beside
+// its scores (rounds, weights, stores) is shared by four. Lane l of a token
+// holds experts 64 i + 8 l + j, i < 2, j < 8, sorts their numbers and keeps the
+// best eight in order; a round is three exchanges and a shift. (Keys that need
+// the error bound lose this way: 65536 x 128 fp32 with bias 37 us, 31 one a warp.)
 constexpr int kManyExperts = 128;
 constexpr uint32_t kManyIndex = kManyExperts - 1;
 
@@ -606,26 +607,18 @@ __device__ __forceinline__ void order_eight(uint32_t (&v)[8]) {
           if (i + j + k < 8 && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order_two(v[i + j], v[i + j + k]);
 }
 
-template <class T, bool VEC, bool BIAS>
-__global__ void __launch_bounds__(32 * kWarps, 1) select_many_kernel(const SelectArgs a) {
+template <class T, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps, 2) select_many_kernel(const SelectArgs a) {
   begin_after_previous();
-  constexpr bool kWhole = sizeof(T) == 2 && !BIAS;
-  constexpr float kFloor = 1.f + 0x1p-8f;
-  constexpr uint32_t kFloorPlace = 1u << 15;
-  extern __shared__ uint64_t keys[];
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 7;
-  uint64_t* const scratch = keys + (size_t)warp * a.E;
-  int* const tally = reinterpret_cast<int*>(keys + (size_t)warps * a.E);
+  extern __shared__ int tally[];
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, l = lane & 7;
   const int step = gridDim.x * warps * 4;
+  int t = (blockIdx.x * warps + (threadIdx.x >> 5)) * 4 + (lane >> 3);
   const T* const all = static_cast<const T*>(a.scores);
-  int t0 = (blockIdx.x * warps + warp) * 4;  // the warp's first token
 
   RawChunk<T> ahead[2];
-  const T low_score = Elem<T>::from(-INFINITY);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) reinterpret_cast<T*>(&ahead[i])[j] = low_score;
+  for (int i = 0; i < 2; ++i) ahead[i] = narrow<T>(chunk_of(-INFINITY));
   auto fetch = [&](int t) {
     if (t >= a.Q) return;
     const T* z = all + t * a.ld;
@@ -641,30 +634,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) select_many_kernel(const Selec
       }
     }
   };
-  fetch(t0 + (lane >> 3));
+  fetch(t);
   if (a.counts) {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) tally[e] = 0;
     __syncthreads();
   }
-  Chunk bias[BIAS ? 2 : 1];
-  float low = 0.f, range = 1.f;
-  if constexpr (BIAS) {
-    float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int e = 64 * i + 8 * l + j;
-        const float b = e < a.E ? a.bias[e] : -INFINITY;
-        bias[i][j] = b == b ? b : -INFINITY;
-        hi = fmaxf(hi, bias[i][j]);
-        lo = bias[i][j] > -INFINITY ? fminf(lo, bias[i][j]) : lo;
-      }
-    hi = warp_max_f(hi);
-    low = fmaxf(-warp_max_f(-lo), hi - kSpread);
-    range = hi + 1.f - low;
-  }
-  const float key_error = a.sigmoid ? 0x1p-21f : 0x1p-21f + 32 * 0x1p-23f;
   // indexes of the lane's experts counted down, two 16-bit halves a register
   uint32_t index[8];
 #pragma unroll
@@ -673,80 +647,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) select_many_kernel(const Selec
     index[i] = (kManyIndex - e) | (kManyIndex - e - 1) << 16;
   }
 
-  for (; t0 < a.Q; t0 += step) {
-    const int t = t0 + (lane >> 3);
-    const bool live = t < a.Q;
-    const T* z = all + (live ? t : t0) * a.ld;
+  // all lanes of a warp make the same turns: the last token of each may lie past the end
+  for (; t - (lane >> 3) < a.Q; t += step) {
     const RawChunk<T> raw[2] = {ahead[0], ahead[1]};
     fetch(t + step);
-
-    auto scores = [&](int i) {  // NaN counts as -inf
-      Chunk c = widen<T>(raw[i]);
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) c[j] = fmaxf(c[j], -INFINITY);
-      return c;
-    };
-    auto sum_of_exp = [&](float m) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const Chunk s = scores(i);
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) sum += s[j] > -INFINITY ? shifted_exp(s[j], m) : 0.f;
-      }
-      return part_sum<8>(sum);
-    };
-    float m = -INFINITY, denom = 1.f;
     uint32_t u[2][8];
-    float number_error = 0.f;
-    if constexpr (kWhole) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t o = ordered16_pair<T>(raw[i].w[j]);
-          u[i][2 * j] = __byte_perm(o, index[4 * i + j], 0x1054);
-          u[i][2 * j + 1] = __byte_perm(o, index[4 * i + j], 0x3276);
-        }
-    } else {
-      Chunk s[2] = {scores(0), scores(1)};
-      if (!BIAS || !a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) m = fmaxf(m, s[i][j]);
-        m = part_max<8>(m);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t o = ordered16_pair<T>(raw[i].w[j]);
+        u[i][2 * j] = __byte_perm(o, index[4 * i + j], 0x1054);
+        u[i][2 * j + 1] = __byte_perm(o, index[4 * i + j], 0x3276);
       }
-      if (BIAS && !a.sigmoid) denom = sum_of_exp(m);
-      if constexpr (BIAS) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            const float p = a.sigmoid ? fast_sigmoid(s[i][j]) : shifted_exp(s[i][j], m) / denom;
-            s[i][j] = s[i][j] > -INFINITY ? p + bias[BIAS ? i : 0][j] : -INFINITY;
-          }
-      } else {
-        float least = INFINITY;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) least = s[i][j] > -INFINITY ? fminf(least, s[i][j]) : least;
-        low = fmaxf(-part_max<8>(-least), m - kSpread);
-        range = m - low;
-      }
-      const float scale = range > 0.f ? __fdividef(1.f - 0x1p-5f, range) : 0.f, offset = fmaf(-low, scale, 1.f + 0x1p-7f);
-      number_error = range * 0x1p-20f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          const uint32_t f = __float_as_uint(fmaxf(fmaf(s[i][j], scale, offset), kFloor));
-          u[i][j] = (f << 9 & ~kManyIndex) | (kManyIndex - (uint32_t)(64 * i + 8 * l + j));
-        }
-    }
-
-    // the lane's best eight in order
+    // the lane's best eight in order: of two descending eights, the larger of each pair from opposite ends
+    // is a bitonic sequence
     uint32_t b[8];
     order_eight(u[0]);
     order_eight(u[1]);
@@ -757,15 +672,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) select_many_kernel(const Selec
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (!(i & k)) order_two(b[i], b[i + k]);
-    auto best_of_all = [&] {
-      uint32_t v = b[0];
-      v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
-      v = max(v, __shfl_xor_sync(0xffffffffu, v, 2));
-      return max(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    };
     uint32_t won = 0u, top = 0u;
     for (int j = 0; j < a.k; ++j) {
-      const uint32_t best = best_of_all();
+      uint32_t best = b[0];
+      best = max(best, __shfl_xor_sync(0xffffffffu, best, 4));
+      best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
+      best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
       if (l == j) won = best;
       if (j == 0) top = best;
       const bool mine = b[0] == best;
@@ -773,43 +685,28 @@ __global__ void __launch_bounds__(32 * kWarps, 1) select_many_kernel(const Selec
       for (int i = 0; i < 7; ++i) b[i] = mine ? b[i + 1] : b[i];
       b[7] = mine ? 0u : b[7];
     }
-    int id = (int)(kManyIndex - (won & kManyIndex));
-    float v;  // the slot's score
-    if constexpr (kWhole) {
-      v = l < a.k ? from_ordered16<T>(won >> 16) : -INFINITY;
-      if (!a.sigmoid) m = from_ordered16<T>(top >> 16);
-    } else {
-      const uint32_t rest = best_of_all();
-      const uint32_t behind = __shfl_down_sync(0xffffffffu, won, 1);
-      const uint32_t next = l + 1 < a.k ? behind : rest;
-      const float need = 2.f * number_error + (BIAS ? 2.f * key_error + 0x1p-21f * (fabsf(low) + range) : 0.f);
-      const bool clear = (float)((won >> 9) - (next >> 9)) * (0x1p-23f * range) > need && won >> 9 > kFloorPlace;
-      const bool held = range < INFINITY && fabsf(low) <= 0x1p14f * range;
-      // (a lane that gave away all it kept no longer knows its next best)
-      uint32_t unsure = __ballot_sync(0xffffffffu, live && ((l < a.k && !(clear && held)) || b[0] == 0u));
-      while (unsure) {  // few tokens: selected again in double, a warp each
-        const int g = (__ffs(unsure) - 1) >> 3;
-        const int again = __shfl_sync(0xffffffffu, select_double<T>(a, t0 + g, scratch), l);
-        if (lane >> 3 == g) id = again;
-        unsure &= ~(0xFFu << (8 * g));
-      }
-      v = live && l < a.k ? clean_score(z[id]) : -INFINITY;
-    }
-    float w;
+    const int id = (int)(kManyIndex - (won & kManyIndex));
+    const float v = l < a.k ? from_ordered16<T>(won >> 16) : -INFINITY, m = from_ordered16<T>(top >> 16);
+    float w = 0.f;
     if (a.renorm) {
-      const float first = part_max<8>(v);
-      float q = 0.f;
       if (v > -INFINITY)
-        q = a.sigmoid ? expf(fminf(v, 0.f) - fminf(first, 0.f)) / (1.f + expf(-fabsf(v))) : shifted_exp(v, first);
-      const float total = part_sum<8>(q);
-      w = total > 0.f ? a.scale * __fdividef(q, total) : 0.f;
+        w = a.sigmoid ? expf(fminf(v, 0.f) - fminf(m, 0.f)) / (1.f + expf(-fabsf(v))) : shifted_exp(v, m);
+      const float total = part_sum<8>(w);
+      w = total > 0.f ? a.scale * __fdividef(w, total) : 0.f;
     } else if (a.sigmoid) {
       w = v > -INFINITY ? a.scale / (1.f + expf(-v)) : 0.f;
     } else {
-      if (!BIAS) denom = sum_of_exp(m);
+      float denom = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Chunk s = widen<T>(raw[i]);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) denom += s[j] > -INFINITY ? shifted_exp(s[j], m) : 0.f;  // not for NaN either
+      }
+      denom = part_sum<8>(denom);
       w = v > -INFINITY ? a.scale * (shifted_exp(v, m) / denom) : 0.f;
     }
-    if (live && l < a.k) {
+    if (t < a.Q && l < a.k) {
       a.ids[(int64_t)t * a.k + l] = id;
       a.weights[(int64_t)t * a.k + l] = w;
       if (a.counts) atomicAdd(tally + id, 1);
@@ -880,7 +777,7 @@ template <class T, int LANES, int NI, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads) select_bwd_kernel(const SelectArgs a) {
   begin_after_previous();
   const int lane = threadIdx.x % LANES;
-  const int t = (blockIdx.x * kBwdThreads + threadIdx.x) / LANES;
+  const int t = blockIdx.x * (kBwdThreads / LANES) + threadIdx.x / LANES;
   const bool live = t < a.Q;
   const T* z = static_cast<const T*>(a.scores) + t * a.ld;
   T* dz = static_cast<T*>(a.grad) + (int64_t)t * a.E;
@@ -993,8 +890,9 @@ bool four_aligned(const void* p, int64_t ld, int E) {
   return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
 }
 
-// Eight lanes a token need fewer instructions, 32 spread few tokens over more of the machine.
-constexpr int kManyTokens = 32768;
+// From here on four tokens a warp are quicker than one (128 experts, k 8, bf16:
+// 2048 tokens 3.0 and 3.3 us, 16384 tokens 5.4 and 10.0).
+constexpr int kManyTokens = 2048;
 
 struct SelectShape {
   int blocks, warps, smem;
@@ -1036,25 +934,20 @@ cudaError_t launch_select(const SelectArgs& a, const SelectShape& s, cudaStream_
   return a.bias ? start_select<T, NI, false, true>(a, s, st) : start_select<T, NI, false, false>(a, s, st);
 }
 
-template <class T, bool VEC, bool BIAS>
-cudaError_t start_many(const SelectArgs& a, int sms, cudaStream_t st) {
-  SelectArgs quarter = a;  // a warp's turn is four tokens
-  quarter.Q = (a.Q + 3) / 4;
-  static std::atomic<unsigned long long> opted{0};
-  return start(select_many_kernel<T, VEC, BIAS>, opted, a, select_shape(quarter, sms), st);
-}
-
 template <class T>
 cudaError_t launch_many(const SelectArgs& a, int sms, cudaStream_t st) {
-  const int type = sizeof(T) == 4 ? RAWINT4_TYPE_F32 : RAWINT4_TYPE_BF16;  // a size
-  if (a.E % kChunk == 0 && rows_aligned(a.scores, a.ld, type))
-    return a.bias ? start_many<T, true, true>(a, sms, st) : start_many<T, true, false>(a, sms, st);
-  return a.bias ? start_many<T, false, true>(a, sms, st) : start_many<T, false, false>(a, sms, st);
+  SelectArgs quarter = a;  // a warp's turn is four tokens
+  quarter.Q = (a.Q + 3) / 4;
+  const SelectShape s = select_shape(quarter, sms);
+  const bool vec = a.E % kChunk == 0 && rows_aligned(a.scores, a.ld, RAWINT4_TYPE_BF16);
+  return launch_early(vec ? select_many_kernel<T, true> : select_many_kernel<T, false>, s.blocks, 32 * s.warps,
+                      a.E * (int)sizeof(int), st, a);
 }
 
 template <class T>
 cudaError_t select_type(const SelectArgs& a, int sms, cudaStream_t st) {
-  if (a.E <= kManyExperts && a.k <= 8 && a.groups == 1 && a.Q >= kManyTokens) return launch_many<T>(a, sms, st);
+  if constexpr (sizeof(T) == 2)
+    if (!a.bias && a.E <= kManyExperts && a.k <= 8 && a.groups == 1 && a.Q >= kManyTokens) return launch_many<T>(a, sms, st);
   const SelectShape s = select_shape(a, sms);
   if (a.E <= 128) return launch_select<T, 1>(a, s, st);
   if (a.E <= 256) return launch_select<T, 2>(a, s, st);
@@ -1076,14 +969,14 @@ cudaError_t launch_bwd(const SelectArgs& a, cudaStream_t st) {
 
 template <class T>
 cudaError_t select_bwd_type(const SelectArgs& a, cudaStream_t st) {
-  const bool few = a.k <= 8 && a.Q >= kManyTokens, all = !a.sigmoid && !a.renorm;
-  if (!all) return few ? launch_bwd<T, 8, 0>(a, st) : launch_bwd<T, 32, 0>(a, st);
-  if (few && a.E <= 128) return launch_bwd<T, 8, 2>(a, st);
-  if (few && a.E <= 256) return launch_bwd<T, 8, 4>(a, st);
+  const bool all = !a.sigmoid && !a.renorm;
+  // eight lanes a token (16384 x 128 fp32, k 8: 6.8 us, with 32 7.6), 32 where a row is longer (8192 x 384:
+  // 6.4 us, with eight 8.5)
+  if (a.k <= 8 && a.E <= 128) return all ? launch_bwd<T, 8, 2>(a, st) : launch_bwd<T, 8, 0>(a, st);
+  if (!all || a.E > 1024) return launch_bwd<T, 32, 0>(a, st);
   if (a.E <= 256) return launch_bwd<T, 32, 1>(a, st);
   if (a.E <= 512) return launch_bwd<T, 32, 2>(a, st);
-  if (a.E <= 1024) return launch_bwd<T, 32, 4>(a, st);
-  return launch_bwd<T, 32, 0>(a, st);
+  return launch_bwd<T, 32, 4>(a, st);
 }
 
 }  // namespace
