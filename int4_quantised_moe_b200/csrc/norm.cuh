@@ -7,10 +7,8 @@ constexpr int kMaxWidth = 16384;
 constexpr int kFewRows = 296;        // two rows an SM
 constexpr int kFwdWarps = 8;         // rows of a forward block when a row lies in one warp
 // Threads of a backward block at most, so that w, dw and db (8 registers a
-// chunk each) and a checkpoint's numbers (4) fit.
-__host__ __device__ constexpr int bwd_threads(int nv, bool bias, bool ckpt) {
-  return nv == 4 ? 512 : nv == 2 && bias ? (ckpt ? 576 : 640) : 896;
-}
+// chunk each) fit: 128, 96 and 72 registers a thread.
+__host__ __device__ constexpr int bwd_threads(int nv) { return nv == 4 ? 512 : nv == 2 ? 640 : 896; }
 constexpr int kBwdBlocks = 148;      // blocks of the backward at most, one an SM: rows of partial sums
 constexpr int kBwdMaxStages = 4;     // rows in a thread group's ring
 constexpr int kBwdRing = 200 * 1024; // bytes of shared memory for the rings
@@ -61,14 +59,15 @@ inline Shape shape_for(int width, int most, int warps_rows) {
   return {most, ceil_div(chunks, most * 32) * 32, 1};
 }
 
-// Backward: four chunks a thread, with db two where the row's threads then fit
-// a block (8192 x 7168 bf16 RMS: 62 us, with two 78; 4096 x 2816 from INT8 with
-// db: 37 us, with two 27).
+// Backward: four chunks a thread, fewer where db needs registers too: two, or
+// one next to a checkpoint's numbers, if the row's threads then fit a block
+// (8192 x 7168 bf16 RMS: four 62 us, two 78; 4095 x 704 fp32 with db: two
+// 13.7 us, one 14.8; 4096 x 2816 from INT8 with db: four 37 us, two 27.5, one 25).
 inline Shape bwd_shape(const NormArgs& a) {
-  const bool ckpt = a.in_codes != nullptr;
-  Shape s = shape_for(a.width, a.want_b ? 2 : 4, 1);
-  if (s.threads > bwd_threads(2, a.want_b, ckpt)) s = shape_for(a.width, 4, 1);
-  s.rows = bwd_threads(s.nv, a.want_b, ckpt) / s.threads;
+  int most = !a.want_b ? 4 : a.in_codes ? 1 : 2;
+  Shape s = shape_for(a.width, most, 1);
+  while (s.threads > bwd_threads(s.nv) / (s.nv == 1 ? 2 : 1)) s = shape_for(a.width, most *= 2, 1);
+  s.rows = bwd_threads(s.nv) / s.threads;
   if (s.threads > 32 && s.rows > 15) s.rows = 15;  // named barriers
   return s;
 }

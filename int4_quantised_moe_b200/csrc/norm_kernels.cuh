@@ -286,7 +286,7 @@ __device__ __forceinline__ void copy_wait_but(int n) {
 // dx; otherwise both reads go to memory (the second finds the row in cache).
 // The scale bytes of a checkpoint are fetched one row ahead into registers.
 template <class T, int NV, bool VEC, int CKPT, bool SUMB, bool LAYER>
-__global__ void __launch_bounds__(bwd_threads(NV, SUMB, CKPT)) norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArgs a) {
   __shared__ float2 buf[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kFormat = CKPT - 1;
