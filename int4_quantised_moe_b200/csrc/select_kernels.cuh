@@ -11,9 +11,10 @@
 // rounds p + bias. Without a bias p grows with s and the scores themselves are
 // compared. With one (and for sums of two keys) the keys are formed in fp32
 // with an error bound. Where the gaps between the best keys exceed the bound
-// the selection stands; the experts whose order is open (about one token in a
-// hundred has some) are ordered again by their keys in double, and a token
-// whose groups are open is selected again in double as a whole.
+// the selection stands; experts or groups whose order is open (about one token
+// in a hundred has some) are ordered again by their keys in double. Tokens that
+// the fp32 form cannot hold (too few scores left, keys out of range) are
+// selected in double as a whole.
 //
 // One warp a token, scores in registers, four neighbours a lane and step. A
 // key becomes one 32-bit number: its place in the range of possible keys (23
@@ -314,11 +315,68 @@ __device__ __noinline__ int order_double(const SelectArgs& a, int t, int e, int 
   return id;
 }
 
-// The group stage: groups outside the groups_kept best are closed (bits of
-// `open` cleared). Returns whether the fp32 keys decide it. `row`: the warp's scratch.
-template <int NP, class Prob>
-__device__ __forceinline__ bool close_groups(const SelectArgs& a, const float (&s)[NP], float* row, int lane,
-                                             float key_error, Prob prob, uint32_t* open) {
+// Of the groups marked in `open` (bit g << share for group g), the `need` best
+// by their scores in double, marked the same way.
+template <class T>
+__device__ __noinline__ uint32_t groups_double(const SelectArgs& a, int t, uint32_t open, int need, int share, float m) {
+  const int lane = threadIdx.x & 31, size = a.E / a.groups;
+  const T* z = static_cast<const T*>(a.scores) + t * a.ld;
+  double denom = 1.0;
+  if (!a.sigmoid) {
+    denom = 0.0;
+    for (int e = lane; e < a.E; e += 32) {
+      const double v = clean_score(z[e]);
+      denom += v == (double)m ? 1.0 : exp(v - (double)m);
+    }
+    denom = warp_sum_d(denom);
+  }
+  auto prob = [&](double s) {
+    return a.sigmoid ? 1.0 / (1.0 + exp(-s)) : (s == (double)m ? 1.0 : exp(s - (double)m)) / denom;
+  };
+  double mine = -INFINITY;  // lane g << share: the score of group g
+  for (uint32_t left = open; left; left &= left - 1) {
+    const int at = __ffs(left) - 1;
+    double b1 = -INFINITY, b2 = -INFINITY;
+    for (int i = lane; i < size; i += 32) {
+      const int e = (at >> share) * size + i;
+      double v = clean_score(z[e]);
+      if (a.bias && v > -INFINITY) {
+        const double b = a.bias[e];
+        v = b == b ? prob(v) + b : -INFINITY;
+      }
+      b2 = fmax(b2, fmin(b1, v));
+      b1 = fmax(b1, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
+      b2 = fmax(fmin(b1, c1), fmax(b2, c2));
+      b1 = fmax(b1, c1);
+    }
+    if (a.group_top > 1) {
+      if (!a.bias) {
+        b1 = b1 > -INFINITY ? prob(b1) : b1;
+        b2 = b2 > -INFINITY ? prob(b2) : b2;
+      }
+      b1 = b2 > -INFINITY ? b1 + b2 : b1;
+    }
+    if (lane == at) mine = b1;
+  }
+  int better = 0;
+  for (uint32_t left = open; left; left &= left - 1) {
+    const int at = __ffs(left) - 1;
+    const double u = __shfl_sync(0xffffffffu, mine, at);
+    better += u > mine || (u == mine && at < lane);
+  }
+  return __ballot_sync(0xffffffffu, (open >> lane & 1u) && better < need);
+}
+
+// The group stage: experts outside the groups_kept best groups are closed (their
+// bits of the result cleared). Groups whose order around the border the fp32
+// keys leave open are ordered in double. `row`: the warp's scratch.
+template <class T, int NP, class Prob>
+__device__ __forceinline__ uint32_t open_experts(const SelectArgs& a, int t, const float (&s)[NP], float* row, int lane,
+                                                 float key_error, float m, Prob prob) {
 #pragma unroll
   for (int i = 0; i < NP; ++i)
     if (expert_at(i, lane) < a.E) row[expert_at(i, lane)] = s[i];
@@ -353,25 +411,31 @@ __device__ __forceinline__ bool close_groups(const SelectArgs& a, const float (&
     const float u = __shfl_sync(0xffffffffu, b1, o << share);
     better += u > b1 || (u == b1 && o < g);
   }
-  const bool in = g < a.groups && better < a.kept;
-  const uint32_t kept = __ballot_sync(0xffffffffu, in);
-  bool sure = true;
+  const bool first = part == 0 && g < a.groups;  // one lane speaks for a group
+  const bool in = first && better < a.kept;
+  uint32_t kept = __ballot_sync(0xffffffffu, in);
   if (a.kept < a.groups && (a.bias || a.group_top > 1)) {
-    const float lo = -warp_max_f(in ? -b1 : -INFINITY), hi = warp_max_f(!in && g < a.groups ? b1 : -INFINITY);
-    const float most = warp_max_f(g < a.groups && magnitude < INFINITY ? magnitude : 0.f);
-    sure = apart(lo, hi, 2.f * key_error, 4.f * most);
+    const float lo = -warp_max_f(in ? -b1 : -INFINITY), hi = warp_max_f(first && !in ? b1 : -INFINITY);
+    const float most = warp_max_f(first && magnitude < INFINITY ? magnitude : 0.f);
+    const bool sure = in ? apart(b1, hi, 2.f * key_error, 4.f * most) : apart(lo, b1, 2.f * key_error, 4.f * most);
+    const uint32_t open = __ballot_sync(0xffffffffu, first && !sure);
+    if (open) {
+      kept &= ~open;
+      kept |= groups_double<T>(a, t, open, a.kept - __popc(kept), share, m);
+    }
   }
   const float inv_size = 1.f / (float)size;  // (e + 0.5) / size truncates to e / size for e < 4096
+  uint32_t mask = 0xffffffffu;
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int of = (int)(((float)expert_at(i, lane) + 0.5f) * inv_size);
-    if (!((kept >> ((of << share) & 31)) & 1u)) *open &= ~(1u << i);
+    if (!((kept >> ((of << share) & 31)) & 1u)) mask &= ~(1u << i);
   }
   __syncwarp();
-  return sure;
+  return mask;
 }
 
-template <class T, int NI, bool VEC, bool BIAS>
+template <class T, int NI, bool VEC, bool BIAS, bool GROUPS>
 __global__ void __launch_bounds__(32 * kWarps, NI <= 4 ? 2 : 1) select_kernel(const SelectArgs a) {
   begin_after_previous();
   constexpr int NP = 4 * NI;
@@ -449,8 +513,8 @@ __global__ void __launch_bounds__(32 * kWarps, NI <= 4 ? 2 : 1) select_kernel(co
     }
     bool sure = true;
     uint32_t open = 0xffffffffu;  // bit i: the lane's expert i lies in a kept group
-    if (a.groups > 1) {
-      sure = close_groups<NP>(a, s, reinterpret_cast<float*>(scratch), lane, key_error, prob, &open);
+    if constexpr (GROUPS) {
+      open = open_experts<T, NP>(a, t, s, reinterpret_cast<float*>(scratch), lane, key_error, m, prob);
       if (!kWhole)
 #pragma unroll
         for (int i = 0; i < NP; ++i) s[i] = open >> i & 1u ? s[i] : -INFINITY;
@@ -462,7 +526,7 @@ __global__ void __launch_bounds__(32 * kWarps, NI <= 4 ? 2 : 1) select_kernel(co
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         u[i] = ordered16<T>(s[i] + 0.f) << 16 | (kIndex - (uint32_t)expert_at(i, lane));
-        if (a.groups > 1) u[i] = open >> i & 1u ? u[i] : 0u;
+        if (GROUPS) u[i] = open >> i & 1u ? u[i] : 0u;
       }
     } else {
       if constexpr (!BIAS) {
@@ -921,17 +985,22 @@ cudaError_t start(K kernel, std::atomic<unsigned long long>& opted, const Select
   return launch_early(kernel, s.blocks, 32 * s.warps, s.smem, st, a);
 }
 
-template <class T, int NI, bool VEC, bool BIAS>
+template <class T, int NI, bool VEC, bool BIAS, bool GROUPS>
 cudaError_t start_select(const SelectArgs& a, const SelectShape& s, cudaStream_t st) {
   static std::atomic<unsigned long long> opted{0};
-  return start(select_kernel<T, NI, VEC, BIAS>, opted, a, s, st);
+  return start(select_kernel<T, NI, VEC, BIAS, GROUPS>, opted, a, s, st);
+}
+
+template <class T, int NI, bool VEC>
+cudaError_t pick_select(const SelectArgs& a, const SelectShape& s, cudaStream_t st) {
+  if (a.groups > 1)
+    return a.bias ? start_select<T, NI, VEC, true, true>(a, s, st) : start_select<T, NI, VEC, false, true>(a, s, st);
+  return a.bias ? start_select<T, NI, VEC, true, false>(a, s, st) : start_select<T, NI, VEC, false, false>(a, s, st);
 }
 
 template <class T, int NI>
 cudaError_t launch_select(const SelectArgs& a, const SelectShape& s, cudaStream_t st) {
-  if (four_aligned<T>(a.scores, a.ld, a.E))
-    return a.bias ? start_select<T, NI, true, true>(a, s, st) : start_select<T, NI, true, false>(a, s, st);
-  return a.bias ? start_select<T, NI, false, true>(a, s, st) : start_select<T, NI, false, false>(a, s, st);
+  return four_aligned<T>(a.scores, a.ld, a.E) ? pick_select<T, NI, true>(a, s, st) : pick_select<T, NI, false>(a, s, st);
 }
 
 template <class T>

@@ -229,6 +229,37 @@ def test_select_ties_and_near_ties(B):
     assert np.array_equal(ids.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_select_equal_scores(B, dtype):
+    """A router at its start: every score the same, with and without groups and a bias of zeros."""
+    z = torch.zeros((40, 96), dtype=DTYPES[dtype])
+    z[20:] = -3.25
+    z[30:, ::2] = -0.0
+    for groups, kept, top in ((1, 1, 1), (8, 3, 2)):
+        for b in (None, torch.zeros(96)):
+            cfg = B.make_select_cfg(96, 8, groups=groups, groups_kept=kept, group_top=top)
+            ids, w = B.router_select(z.cuda(), cfg, None if b is None else b.cuda())
+            want, ow = oselect.forward(f64(z), 8, "sigmoid", None if b is None else f64(b), groups, kept, top)
+            assert np.array_equal(ids.cpu().numpy(), want)
+            close(w, ow, share_tolerance(z, 8) * ow)
+
+
+def test_select_past_32_bit_offsets(B):
+    """Rows 2^32 elements into a buffer of scores."""
+    pitch, rows = 1 << 20, 4200
+    buf = torch.empty((rows, pitch), dtype=torch.bfloat16, device="cuda")
+    z = buf[:, :64]
+    z.copy_(torch.randn((rows, 64), generator=torch.Generator().manual_seed(6)))
+    dense = z.contiguous()
+    gr = torch.randn((rows, 4), generator=torch.Generator().manual_seed(7)).cuda()
+    for score, bias in (("softmax", None), ("sigmoid", torch.linspace(-0.1, 0.1, 64, device="cuda"))):
+        cfg = B.make_select_cfg(64, 4, score=score, renormalise=False)
+        ids, w = B.router_select(z, cfg, bias)
+        ids2, w2 = B.router_select(dense, cfg, bias)
+        assert torch.equal(ids, ids2) and torch.equal(w, w2)
+        assert torch.equal(B.router_select_bwd(z, cfg, ids, gr), B.router_select_bwd(dense, cfg, ids2, gr))
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("groups", [1, 4])
