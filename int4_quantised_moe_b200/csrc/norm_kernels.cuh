@@ -33,20 +33,21 @@ __device__ __forceinline__ int column(int i, int j, int t, int threads) {
 template <bool VEC>
 __device__ __forceinline__ Chunk load_vector(const void* p, int type, int i, int t, int threads, int width, float none) {
   if (!p) return chunk_of(none);
-  if (VEC) {
+  if constexpr (VEC) {
     const int c = column<true>(i, 0, t, threads);
     if (c >= width) return chunk_of(0.f);
     if (type == RAWINT4_TYPE_F32) return widen<float>(load_chunk(static_cast<const float*>(p) + c));
     if (type == RAWINT4_TYPE_BF16) return widen<__nv_bfloat16>(load_chunk(static_cast<const __nv_bfloat16*>(p) + c));
     return widen<__half>(load_chunk(static_cast<const __half*>(p) + c));
-  }
-  Chunk v;
+  } else {
+    Chunk v;
 #pragma unroll
-  for (int j = 0; j < kChunk; ++j) {
-    const int c = column<false>(i, j, t, threads);
-    v[j] = c < width ? load_as(p, type, c) : 0.f;
+    for (int j = 0; j < kChunk; ++j) {
+      const int c = column<false>(i, j, t, threads);
+      v[j] = c < width ? load_as(p, type, c) : 0.f;
+    }
+    return v;
   }
-  return v;
 }
 
 // Chunk i of a row in memory, in the scalar layout; columns past the width read as 0.

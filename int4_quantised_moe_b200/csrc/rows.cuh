@@ -316,8 +316,8 @@ __device__ __forceinline__ Chunk ckpt_decode8(uint2 w, uint32_t byte, int fmt) {
 // before it in the stream is complete and visible; it also lets the next
 // kernel's blocks take the places that this one's last blocks leave.
 __device__ __forceinline__ void begin_after_previous() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // after the wait: one kernel ahead, no more
 }
 
 __device__ __forceinline__ float row_warp_sum(float v) {

@@ -75,10 +75,13 @@ __device__ __forceinline__ float part_sum(float v) {
 }
 template <int LANES>
 __device__ __forceinline__ float part_max(float v) {
-  if (LANES == 32) return warp_max_f(v);
+  if constexpr (LANES == 32) {
+    return warp_max_f(v);
+  } else {
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
 }
 
 // Two of them at once (NaN becomes -inf, -0 becomes +0), and back.
