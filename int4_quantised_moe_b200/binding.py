@@ -497,6 +497,7 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 CKPT_FORMATS = {"e4m3": 0, "int8": 1}
 NORM_KINDS = {"layer": 0, "rms": 1}
 CKPT_GROUP = 32  # columns under one scale of a checkpoint
+_INT32_MAX = (1 << 31) - 1  # sizes travel as int32; the library has lower limits of its own
 
 
 def _elsewhere(device: torch.device, stream, *tensors):
@@ -508,6 +509,8 @@ def _elsewhere(device: torch.device, stream, *tensors):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    if device.index == torch._C._cuda_getDevice() and stream.cuda_stream == _here(device):
+        return None
     for t in tensors:
         if isinstance(t, Ckpt8):
             t.codes.record_stream(stream)
@@ -539,6 +542,8 @@ def _rows(t, name: str, width: Optional[int] = None, device: Optional[torch.devi
     shape = t.shape
     if len(shape) != 2 or (width is not None and shape[1] != width):
         raise ValueError(f"{name}: expected shape [rows, {'width' if width is None else width}], got {tuple(shape)}")
+    if max(shape) > _INT32_MAX:
+        raise ValueError(f"{name}: shape {tuple(shape)} has a size above {_INT32_MAX}")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
     if device is not None and t.device != device:
@@ -638,6 +643,8 @@ class Ckpt8:
         if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
             raise ValueError(f"{name}.codes: expected a uint8 tensor [rows, width]")
         rows, width = codes.shape
+        if max(rows, width) > _INT32_MAX:
+            raise ValueError(f"{name}.codes: shape {tuple(codes.shape)} has a size above {_INT32_MAX}")
         _expect(codes, f"{name}.codes", torch.uint8, (rows, width), device)
         _expect(self.scales, f"{name}.scales", torch.uint8, (rows, -(-width // CKPT_GROUP)), codes.device)
         return fmt

@@ -153,6 +153,13 @@ def test_binding_refuses_wrong_tensors(B):
         B.ckpt8_save(x, "e5m2")
     with pytest.raises(ValueError, match="CUDA tensor"):
         B.ckpt8_save(x)
+    huge = torch.zeros((1, 64)).expand(1 << 31, 64)  # a size that int32 would wrap
+    for call in (lambda: B.router_select(huge, cfg), lambda: B.ckpt8_save(huge), lambda: B.norm_fwd(huge),
+                 lambda: B.norm_bwd(x, huge, x[:, 0])):
+        with pytest.raises(ValueError, match="above 2147483647"):
+            call()
+    with pytest.raises(ValueError, match="above 2147483647"):
+        B.ckpt8_load(B.Ckpt8(torch.zeros((1, 64), dtype=torch.uint8).expand(1 << 31, 64), x, "int8"))
     codes, scales = torch.zeros((4, 64), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8)
     with pytest.raises(ValueError, match="CUDA tensor"):
         B.ckpt8_load(B.Ckpt8(codes, scales, "int8"))

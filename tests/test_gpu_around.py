@@ -433,6 +433,11 @@ NORM = [
     (5, 512, "rms", "bf16", "fp32", False, True, 0),
     (2000, 4096, "rms", "bf16", "bf16", True, True, 0),
     (450, 8192, "layer", "fp16", "fp16", True, True, 0),
+    (300, 512, "layer", "fp32", "bf16", True, True, 0),
+    (33, 96, "rms", "bf16", "fp16", True, True, 8),
+    (700, 400, "rms", "bf16", "fp32", True, False, 0),
+    (12, 12288, "layer", "bf16", "bf16", True, True, 0),
+    (12, 12288, "rms", "fp32", "fp32", True, False, 0),
 ]
 
 
@@ -497,7 +502,7 @@ def test_norm_forward_and_backward(B, case):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("case", [NORM[i] for i in (0, 1, 3, 4, 5, 6, 7, 10, 13, 14, 17)],
+@pytest.mark.parametrize("case", [NORM[i] for i in (0, 1, 3, 4, 5, 6, 7, 10, 13, 14, 17, 20, 21, 22)],
                          ids=lambda c: f"{c[0]}x{c[1]}-{c[2]}-{c[3]}")
 def test_norm_from_a_checkpoint(B, case, fmt):
     """Saving in the forward's pass writes the codes of ckpt8_save; the recomputed forward and the
@@ -672,6 +677,12 @@ def test_a_stream_of_ones_own(B):
     with torch.cuda.stream(s):
         got = _pass(B, z, cfg, bias, gr, x, w, gy)
     s.synchronize()
+    graph = torch.cuda.CUDAGraph()  # captured on a stream that the calls name as well
+    with torch.cuda.graph(graph, stream=s):
+        held = B.norm_bwd(gy, B.ckpt8_save(x, "int8", stream=s), rstd, w, stream=s)[0]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(held, want[5])
     for a, b in zip(got, want):
         assert torch.equal(a, b)
 
