@@ -656,6 +656,46 @@ def test_two_graphs_replayed_at_once(B):
                 assert torch.equal(a, b)
 
 
+def test_capture_behind_copies_fills_and_other_streams(B):
+    """The kernels start early behind one another; behind a copy, a fill, a host-pinned upload or a join with
+    another stream in the same capture they wait like any kernel."""
+    cfg = B.make_select_cfg(128, 8)
+    z, bias, gr, x, w, gy = _operands(21)
+    pinned = x.cpu().pin_memory()
+    z2, x2, x3 = torch.empty_like(z), torch.empty_like(x), torch.empty_like(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z2.copy_(z)
+        ids, wt = B.router_select(z2, cfg, bias)
+        x3.zero_()
+        x3.copy_(pinned, non_blocking=True)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            x2.copy_(x)
+            ck = B.ckpt8_save(x2, "e4m3")
+        y, _, rstd, _ = B.norm_fwd(x3, w)
+        torch.cuda.current_stream().wait_stream(side)
+        dx, dw, _ = B.norm_bwd(gy, ck, rstd, w)
+        back = B.ckpt8_load(ck)
+    for seed in (22, 23):
+        fresh = _operands(seed)
+        for a, b in zip((z, bias, gr, x, w, gy), fresh):
+            a.copy_(b)
+        pinned.copy_(fresh[3])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want_ck = B.ckpt8_save(x, "e4m3")
+        want_y, _, want_rstd, _ = B.norm_fwd(x, w)
+        want_ids, want_wt = B.router_select(z, cfg, bias)
+        want_dx, want_dw, _ = B.norm_bwd(gy, want_ck, want_rstd, w)
+        for a, b in ((ids, want_ids), (wt, want_wt), (y, want_y), (ck.codes, want_ck.codes), (dx, want_dx), (dw, want_dw),
+                     (back, B.ckpt8_load(want_ck))):
+            assert torch.equal(a, b)
+
+
 def test_a_stream_of_ones_own(B):
     """The same pass on a side stream, given by object, by handle, or made current."""
     cfg = B.make_select_cfg(128, 8)
