@@ -117,14 +117,14 @@ RAWINT4_API int rawint4_norm_fwd(const rawint4_norm_cfg* cfg, const void* x, int
   a.codes = save_codes;
   a.scales = save_scales;
   a.fmt = save_format;
-  const bool vec = input_aligned(a, cfg->type) && rows_aligned(y, a.width, cfg->type) && aligned16(weight) &&
+  a.vec = input_aligned(a, cfg->type) && rows_aligned(y, a.width, cfg->type) && aligned16(weight) &&
                    aligned16(bias) && reinterpret_cast<uintptr_t>(save_codes) % 8 == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream_);
   R4_PROF("norm_fwd", st);
   cudaError_t err;
-  if (cfg->type == RAWINT4_TYPE_F32) err = run_norm_fwd<float>(a, cfg->type, vec, st);
-  else if (cfg->type == RAWINT4_TYPE_BF16) err = run_norm_fwd<__nv_bfloat16>(a, cfg->type, vec, st);
-  else err = run_norm_fwd<__half>(a, cfg->type, vec, st);
+  if (cfg->type == RAWINT4_TYPE_F32) err = run_norm_fwd<float>(a, cfg->type, st);
+  else if (cfg->type == RAWINT4_TYPE_BF16) err = run_norm_fwd<__nv_bfloat16>(a, cfg->type, st);
+  else err = run_norm_fwd<__half>(a, cfg->type, st);
   return err == cudaSuccess ? RAWINT4_OK : RAWINT4_CUDA_ERROR;
 }
 
@@ -169,13 +169,13 @@ RAWINT4_API int rawint4_norm_bwd(const rawint4_norm_cfg* cfg, const void* x, int
   a.want_b = grad_bias != nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream_);
   if (a.rows > 0) {
-    const bool vec = input_aligned(a, cfg->type) && rows_aligned(grad_y, ldg, cfg->type) &&
+    a.vec = input_aligned(a, cfg->type) && rows_aligned(grad_y, ldg, cfg->type) &&
                      rows_aligned(grad_x, a.width, cfg->type) && aligned16(weight);
     R4_PROF("norm_bwd", st);
     cudaError_t err;
-    if (cfg->type == RAWINT4_TYPE_F32) err = run_norm_bwd<float>(a, cfg->type, vec, st);
-    else if (cfg->type == RAWINT4_TYPE_BF16) err = run_norm_bwd<__nv_bfloat16>(a, cfg->type, vec, st);
-    else err = run_norm_bwd<__half>(a, cfg->type, vec, st);
+    if (cfg->type == RAWINT4_TYPE_F32) err = run_norm_bwd<float>(a, cfg->type, st);
+    else if (cfg->type == RAWINT4_TYPE_BF16) err = run_norm_bwd<__nv_bfloat16>(a, cfg->type, st);
+    else err = run_norm_bwd<__half>(a, cfg->type, st);
     if (err != cudaSuccess) return RAWINT4_CUDA_ERROR;
   }
   if (sums) {

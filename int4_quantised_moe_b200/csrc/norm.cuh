@@ -20,6 +20,7 @@ struct NormArgs {
   int64_t ldx;
   int in_fmt;
   int rows, width, groups;
+  int vec;                  // every row, weight and bias may move with vector accesses
   int layer;                // subtract the mean
   int w_type;
   float eps;
@@ -59,6 +60,11 @@ inline Shape shape_for(int width, int most, int warps_rows) {
   return {most, ceil_div(chunks, most * 32) * 32, 1};
 }
 
+// The forward's scalar layout has a fixed number of threads a row, so that a
+// thread's elements lie at constant distances: 32 up to 256 columns, 128 up to
+// 2048, else 512 (8192 x 2817 bf16: 80 us, with the vector layout's counts 94).
+__host__ __device__ constexpr int any_threads(int nv) { return nv == 1 ? 32 : nv == 2 ? 128 : 512; }
+
 // Backward: four chunks a thread, fewer where db needs registers too: two, or
 // one next to a checkpoint's numbers, if the row's threads then fit a block
 // (8192 x 7168 bf16 RMS: four 62 us, two 78; 4095 x 704 fp32 with db: two
@@ -77,11 +83,10 @@ inline int bwd_blocks(const Shape& s, int rows) {
   return need < kBwdBlocks ? need : kBwdBlocks;
 }
 
-// The kernels for one element type (norm_fwd.cu, norm_bwd_f32.cu, norm_bwd_bf16.cu, norm_bwd_f16.cu);
-// `vec`: every row, weight and bias may move with vector accesses. a.rows > 0.
+// The kernels for one element type (norm_fwd.cu, norm_bwd_f32.cu, norm_bwd_bf16.cu, norm_bwd_f16.cu). a.rows > 0.
 template <class T>
-cudaError_t run_norm_fwd(const NormArgs& a, int type, bool vec, cudaStream_t st);
+cudaError_t run_norm_fwd(const NormArgs& a, int type, cudaStream_t st);
 template <class T>
-cudaError_t run_norm_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st);
+cudaError_t run_norm_bwd(const NormArgs& a, int type, cudaStream_t st);
 
 }  // namespace r4

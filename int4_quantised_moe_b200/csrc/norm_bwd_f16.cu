@@ -4,8 +4,8 @@
 namespace r4 {
 
 template <>
-cudaError_t run_norm_bwd<__half>(const NormArgs& a, int type, bool vec, cudaStream_t st) {
-  return bwd_type<__half>(a, type, vec, st);
+cudaError_t run_norm_bwd<__half>(const NormArgs& a, int type, cudaStream_t st) {
+  return bwd_type<__half>(a, type, st);
 }
 
 }  // namespace r4

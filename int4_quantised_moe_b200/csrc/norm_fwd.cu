@@ -4,16 +4,16 @@
 namespace r4 {
 
 template <>
-cudaError_t run_norm_fwd<float>(const NormArgs& a, int type, bool vec, cudaStream_t st) {
-  return fwd_type<float>(a, type, vec, st);
+cudaError_t run_norm_fwd<float>(const NormArgs& a, int type, cudaStream_t st) {
+  return fwd_type<float>(a, type, st);
 }
 template <>
-cudaError_t run_norm_fwd<__nv_bfloat16>(const NormArgs& a, int type, bool vec, cudaStream_t st) {
-  return fwd_type<__nv_bfloat16>(a, type, vec, st);
+cudaError_t run_norm_fwd<__nv_bfloat16>(const NormArgs& a, int type, cudaStream_t st) {
+  return fwd_type<__nv_bfloat16>(a, type, st);
 }
 template <>
-cudaError_t run_norm_fwd<__half>(const NormArgs& a, int type, bool vec, cudaStream_t st) {
-  return fwd_type<__half>(a, type, vec, st);
+cudaError_t run_norm_fwd<__half>(const NormArgs& a, int type, cudaStream_t st) {
+  return fwd_type<__half>(a, type, st);
 }
 
 }  // namespace r4

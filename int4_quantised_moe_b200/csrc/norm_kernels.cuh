@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
   constexpr bool kScaled = VEC && CKPT;
   constexpr int kFormat = CKPT - 1;
   begin_after_previous();
-  const int t = threadIdx.x, threads = blockDim.x;
+  const int t = threadIdx.x, threads = VEC ? blockDim.x : any_threads(NV);
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps leave; a block-wide row never does
   const int stride = threads * kChunk;  // from a thread's chunk to its next one, in the vector layout
@@ -168,13 +168,15 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
       x[i].w[0] = codes.x;  // decoded once all loads are on their way
       x[i].w[1] = codes.y;
     } else if constexpr (CKPT) {
-      x[i] = narrow<R>(any_ckpt_chunk(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, kFormat,
-                                      i, t, threads, a.width));
+      x[i] = RawChunk<R>{};
+      if (in[i]) x[i] = narrow<R>(any_ckpt_chunk(a.in_codes + (int64_t)row * a.width, a.in_scales + (int64_t)row * a.groups, kFormat,
+                                                 i, t, threads, a.width));
     } else if constexpr (VEC) {
       x[i] = RawChunk<R>{};
       if (in[i]) x[i] = load_chunk(static_cast<const T*>(a.x) + row * a.ldx + t * kChunk + i * stride);
     } else {
-      x[i] = narrow<R>(any_chunk(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width));
+      x[i] = RawChunk<R>{};
+      if (in[i]) x[i] = narrow<R>(any_chunk(static_cast<const T*>(a.x) + row * a.ldx, i, t, threads, a.width));
     }
   }
   if constexpr (kScaled) {
@@ -184,8 +186,9 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
   if (!CKPT && a.codes)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      save_chunk<R, VEC>(x[i], a.codes + (int64_t)row * a.width, a.scales + (int64_t)row * a.groups, a.fmt, i, t, threads,
-                         a.width);
+      if (VEC || __any_sync(0xffffffffu, in[i]))
+        save_chunk<R, VEC>(x[i], a.codes + (int64_t)row * a.width, a.scales + (int64_t)row * a.groups, a.fmt, i, t,
+                           threads, a.width);
 
   const float inv_n = 1.0f / (float)a.width;
   float mu = 0.f;
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
     mu = row_sum(s.x + s.y, threads, 1, buf[0]) * inv_n;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (VEC && !in[i]) continue;
+      if (!in[i]) continue;
       Chunk d = widen<R>(x[i]);
 #pragma unroll
       for (int j = 0; j < kChunk / 2; ++j)
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
     const W* const b = static_cast<const W*>(a.bias);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (VEC && !in[i]) continue;
+      if (!in[i]) continue;
       Chunk v = widen<R>(x[i]);
       const float2 rx = both(kScaled ? r * scale[kScaled ? i : 0] : r);
 #pragma unroll
@@ -479,12 +482,17 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
 
 // ------------------------------------------------------------- launch shapes
 // Forward: eight chunks of a 16-bit row a thread keep a block's warps, and the
-// time they wait for one another, few (8192 x 7168 bf16: 40 us, with four 45);
-// a checkpoint's eight do not fit the registers (4096 x 2816 from INT8: 16 us,
-// with four 11.5). Few rows want many threads each (1 x 7168: eight chunks
-// 3.8 us, four 3.0, two 2.5).
-Shape fwd_shape(const NormArgs& a, int type, bool vec) {
-  int most = vec && !a.in_codes && type != RAWINT4_TYPE_F32 ? 8 : 4;
+// time they wait for one another, few (8192 x 7168 bf16 RMS: 38 us, with four
+// 45); with a mean (layer norm with bias: 63 us, with four 50) or a checkpoint's
+// numbers (4096 x 2816 from INT8: 16 us, with four 11) eight do not fit the
+// registers. Few rows want many threads each (1 x 7168: eight chunks 3.8 us,
+// four 3.0, two 2.5).
+Shape fwd_shape(const NormArgs& a, int type) {
+  if (!a.vec) {
+    const int nv = a.width <= 256 ? 1 : a.width <= 2048 ? 2 : 4;
+    return {nv, any_threads(nv), nv == 1 && a.rows > kFewRows ? kFwdWarps : 1};
+  }
+  int most = !a.in_codes && type != RAWINT4_TYPE_F32 && !a.layer ? 8 : 4;
   if (a.rows <= kFewRows && a.width <= 2 * kChunk * 512) most = 2;
   return shape_for(a.width, most, a.rows <= kFewRows ? 1 : kFwdWarps);
 }
@@ -534,8 +542,9 @@ cudaError_t pick_fwd(const NormArgs& a, const Shape& s, bool vec, cudaStream_t s
 }
 
 template <class T>
-cudaError_t fwd_type(const NormArgs& a, int type, bool vec, cudaStream_t st) {
-  const Shape s = fwd_shape(a, type, vec);
+cudaError_t fwd_type(const NormArgs& a, int type, cudaStream_t st) {
+  const Shape s = fwd_shape(a, type);
+  const bool vec = a.vec;
   if constexpr (sizeof(T) == 2)
     if (s.nv == 8) return launch_fwd<T, T, 8, true, 0>(a, s, st);
   if (s.nv == 1) return pick_fwd<T, 1>(a, s, vec, st);
@@ -565,7 +574,8 @@ cudaError_t pick_bwd(const NormArgs& a, int type, bool vec, cudaStream_t st) {
 }
 
 template <class T>
-cudaError_t bwd_type(const NormArgs& a, int type, bool vec, cudaStream_t st) {
+cudaError_t bwd_type(const NormArgs& a, int type, cudaStream_t st) {
+  const bool vec = a.vec;
   const int nv = bwd_shape(a).nv;
   if (nv == 1) return pick_bwd<T, 1>(a, type, vec, st);
   if (nv == 2) return pick_bwd<T, 2>(a, type, vec, st);
