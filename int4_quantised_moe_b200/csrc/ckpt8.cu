@@ -60,57 +60,36 @@ __global__ void __launch_bounds__(kThreads) ckpt8_save_vec(const T* __restrict__
   }
 }
 
-// Scalar layout: a warp takes kAnyUnroll neighbouring groups of n in all and
-// walks from one to the next, so that it divides once.
+// Scalar layout: a warp takes a segment of a row, up to kAnyUnroll groups that
+// lie at constant distances; n segments, `segments` a row.
 constexpr int kAnyUnroll = 8;
-
-struct Walk {
-  int64_t x, code;  // the lane's element of the group at hand
-  int group, col;
-  int64_t next_x, next_code;  // from a row's last group to the next row's first
-  __device__ __forceinline__ Walk(uint32_t i, uint32_t groups, int width, int64_t ldx, int lane) {
-    const uint32_t row = i / groups;
-    group = (int)(i - row * groups);
-    col = group * kCkptGroup + lane;
-    x = row * ldx + col;
-    code = (int64_t)row * width + col;
-    next_x = ldx - (int64_t)(groups - 1) * kCkptGroup;
-    next_code = width - (int64_t)(groups - 1) * kCkptGroup;
-  }
-  __device__ __forceinline__ void step(int groups, int lane) {
-    const bool wrap = ++group == groups;
-    x += wrap ? next_x : kCkptGroup;
-    code += wrap ? next_code : kCkptGroup;
-    col = wrap ? lane : col + kCkptGroup;
-    group = wrap ? 0 : group;
-  }
-};
 
 template <class T, int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt8_save_any(const T* __restrict__ x, int64_t ldx, int64_t n, int width,
                                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                           int groups) {
+                                                           uint32_t segments, int groups) {
   begin_after_previous();
   const int lane = threadIdx.x & 31;
-  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kAnyUnroll;
-  if (i0 >= n) return;
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (i >= n) return;
+  const uint32_t row = (uint32_t)i / segments;
+  const int g0 = (int)((uint32_t)i - row * segments) * kAnyUnroll;
+  const int col = g0 * kCkptGroup + lane;
+  x += row * ldx + col;
+  codes += (int64_t)row * width + col;
+  const int left = width - col;  // columns from the lane's first one on
   float f[kAnyUnroll];
-  Walk at((uint32_t)i0, groups, width, ldx, lane);
 #pragma unroll
-  for (int u = 0; u < kAnyUnroll; ++u) {
-    f[u] = i0 + u < n && at.col < width ? Elem<T>::to(x[at.x]) : 0.f;
-    at.step(groups, lane);
-  }
-  at = Walk((uint32_t)i0, groups, width, ldx, lane);
+  for (int u = 0; u < kAnyUnroll; ++u) f[u] = u * kCkptGroup < left ? Elem<T>::to(x[u * kCkptGroup]) : 0.f;
   uint32_t mine = 0;  // lane u: the scale byte of group u
 #pragma unroll
   for (int u = 0; u < kAnyUnroll; ++u) {
+    if (g0 + u >= groups) break;
     const uint32_t byte = ckpt_scale_byte(__reduce_max_sync(0xffffffffu, finite_abs_bits(f[u])), FMT);
-    if (i0 + u < n && at.col < width) codes[at.code] = (uint8_t)ckpt_code(f[u], ckpt_inv_scale(byte), FMT);
+    if (u * kCkptGroup < left) codes[u * kCkptGroup] = (uint8_t)ckpt_code(f[u], ckpt_inv_scale(byte), FMT);
     if (lane == u) mine = byte;
-    at.step(groups, lane);
   }
-  if (lane < kAnyUnroll && i0 + lane < n) scales[i0 + lane] = (uint8_t)mine;
+  if (lane < kAnyUnroll && g0 + lane < groups) scales[(int64_t)row * groups + g0 + lane] = (uint8_t)mine;
 }
 
 template <class T, int FMT>
@@ -148,26 +127,28 @@ __global__ void __launch_bounds__(kThreads) ckpt8_load_vec(const uint8_t* __rest
 template <class T, int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt8_load_any(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales, int64_t n, int width,
-                                                           int groups, T* __restrict__ out) {
+                                                           uint32_t segments, int groups, T* __restrict__ out) {
   begin_after_previous();
   const int lane = threadIdx.x & 31;
-  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kAnyUnroll;
-  if (i0 >= n) return;
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (i >= n) return;
+  const uint32_t row = (uint32_t)i / segments;
+  const int g0 = (int)((uint32_t)i - row * segments) * kAnyUnroll;
+  const int col = g0 * kCkptGroup + lane;
+  codes += (int64_t)row * width + col;
+  out += (int64_t)row * width + col;
+  const int left = width - col;
+  const uint32_t mine = lane < kAnyUnroll && g0 + lane < groups ? scales[(int64_t)row * groups + g0 + lane] : 1u;
   uint32_t code[kAnyUnroll];
-  const uint32_t mine = lane < kAnyUnroll && i0 + lane < n ? scales[i0 + lane] : 1u;
-  Walk at((uint32_t)i0, groups, width, width, lane);
+#pragma unroll
+  for (int u = 0; u < kAnyUnroll; ++u) code[u] = u * kCkptGroup < left ? codes[u * kCkptGroup] : 0u;
 #pragma unroll
   for (int u = 0; u < kAnyUnroll; ++u) {
-    code[u] = i0 + u < n && at.col < width ? codes[at.code] : 0u;
-    at.step(groups, lane);
-  }
-  at = Walk((uint32_t)i0, groups, width, width, lane);
-#pragma unroll
-  for (int u = 0; u < kAnyUnroll; ++u) {
-    const float scale = ckpt_scale(__shfl_sync(0xffffffffu, mine, u));
-    if (i0 + u < n && at.col < width)
-      out[at.code] = Elem<T>::from(ckpt_saturate(ckpt_value(code[u], scale, FMT), Elem<T>::kMax));
-    at.step(groups, lane);
+    if (g0 + u >= groups) break;
+    const uint32_t byte = __shfl_sync(0xffffffffu, mine, u);
+    float v = ckpt_value(code[u], ckpt_scale(byte), FMT);
+    if (byte > ckpt_safe_byte<T>(FMT)) v = ckpt_saturate(v, Elem<T>::kMax);
+    if (u * kCkptGroup < left) out[u * kCkptGroup] = Elem<T>::from(v);
   }
 }
 
@@ -187,7 +168,9 @@ cudaError_t slices(int64_t rows, int64_t per_row, int64_t per_block, F run) {
 
 constexpr int kGroupChunks = kCkptGroup / kChunk;
 constexpr int kVecUnits = kThreads * kUnroll;       // chunks of a block
-constexpr int kAnyUnits = kThreads / 32 * kAnyUnroll;  // groups of a block
+constexpr int kAnyUnits = kThreads / 32;        // segments of a block
+
+int segments_of(int groups) { return (groups + kAnyUnroll - 1) / kAnyUnroll; }
 
 uint32_t chunks_per_row(int width, int64_t ld) {
   return ld == width && width % kCkptGroup == 0 ? 0u : (uint32_t)ckpt_groups(width) * kGroupChunks;
@@ -203,9 +186,9 @@ cudaError_t save(int type, const void* x, int64_t ldx, int64_t rows, int width, 
       return launch_early(ckpt8_save_vec<T, FMT>, blocks, kThreads, 0, st, p + r * ldx, ldx, n, width, chunks_per_row(width, ldx),
                                                           codes + r * width, scales + r * groups, groups);
     });
-  return slices(rows, groups, kAnyUnits, [&](int64_t r, int64_t n, unsigned blocks) {
+  return slices(rows, segments_of(groups), kAnyUnits, [&](int64_t r, int64_t n, unsigned blocks) {
     return launch_early(ckpt8_save_any<T, FMT>, blocks, kThreads, 0, st, p + r * ldx, ldx, n, width, codes + r * width,
-                        scales + r * groups, groups);
+                        scales + r * groups, (uint32_t)segments_of(groups), groups);
   });
 }
 
@@ -219,9 +202,9 @@ cudaError_t load(int type, const uint8_t* codes, const uint8_t* scales, int64_t 
       return launch_early(ckpt8_load_vec<T, FMT>, blocks, kThreads, 0, st, codes + r * width, scales + r * groups, n, width,
                                                           chunks_per_row(width, width), groups, p + r * width);
     });
-  return slices(rows, groups, kAnyUnits, [&](int64_t r, int64_t n, unsigned blocks) {
+  return slices(rows, segments_of(groups), kAnyUnits, [&](int64_t r, int64_t n, unsigned blocks) {
     return launch_early(ckpt8_load_any<T, FMT>, blocks, kThreads, 0, st, codes + r * width, scales + r * groups, n, width,
-                        groups, p + r * width);
+                        (uint32_t)segments_of(groups), groups, p + r * width);
   });
 }
 

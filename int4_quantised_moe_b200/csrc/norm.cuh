@@ -60,17 +60,12 @@ inline Shape shape_for(int width, int most, int warps_rows) {
   return {most, ceil_div(chunks, most * 32) * 32, 1};
 }
 
-// The forward's scalar layout has a fixed number of threads a row, so that a
-// thread's elements lie at constant distances: 32 up to 256 columns, 128 up to
-// 2048, else 512 (8192 x 2817 bf16: 80 us, with the vector layout's counts 94).
-__host__ __device__ constexpr int any_threads(int nv) { return nv == 1 ? 32 : nv == 2 ? 128 : 512; }
-
 // Backward: four chunks a thread, fewer where db needs registers too: two, or
 // one next to a checkpoint's numbers, if the row's threads then fit a block
 // (8192 x 7168 bf16 RMS: four 62 us, two 78; 4095 x 704 fp32 with db: two
 // 13.7 us, one 14.8; 4096 x 2816 from INT8 with db: four 37 us, two 27.5, one 25).
 inline Shape bwd_shape(const NormArgs& a) {
-  int most = !a.want_b ? 4 : a.in_codes ? 1 : 2;
+  int most = !a.vec ? 1 : !a.want_b ? 4 : a.in_codes ? 1 : 2;
   Shape s = shape_for(a.width, most, 1);
   while (s.threads > bwd_threads(s.nv) / (s.nv == 1 ? 2 : 1)) s = shape_for(a.width, most *= 2, 1);
   s.rows = bwd_threads(s.nv) / s.threads;
