@@ -287,7 +287,8 @@ __device__ __forceinline__ void copy_wait_but(int n) {
 // blockDim = (threads of a row, row groups); each group walks rows on its own
 // and meets at its own barrier. VEC: a thread's chunks of x and dy of a row lie
 // in its slots of the ring and are read from there twice, for the sums and for
-// dx; otherwise both reads go to memory (the second finds the row in cache).
+// dx; otherwise they are read from memory (a row ahead into registers where a
+// thread has one chunk, else twice, the second time from cache).
 // The scale bytes of a checkpoint are fetched one row ahead into registers.
 template <class T, int NV, bool VEC, int CKPT, bool SUMB, bool LAYER>
 __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArgs a) {
@@ -383,9 +384,49 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
   fetch_stats(first);
   T* out = static_cast<T*>(a.gx) + (int64_t)first * a.width;
 
+  // the scalar layout with one chunk a thread: the next row's elements, as they come, wait in registers
+  constexpr bool kKept = !VEC && NV == 1;
+  constexpr int kAhead = kKept ? kChunk : 1, kAheadX = kKept && !CKPT ? kChunk : 1, kAheadC = kKept && CKPT ? kChunk : 1;
+  T ahead_g[kAhead], ahead_x[kAheadX];
+  uint8_t ahead_code[kAheadC], ahead_byte[kAheadC];
+  auto fetch_any = [&](int row) {
+    if (row >= a.rows) return;
+    const T* const g = static_cast<const T*>(a.gy) + row * a.ldg;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = column<false>(0, j, t, threads);
+      if (c >= a.width) continue;
+      ahead_g[j] = g[c];
+      if constexpr (CKPT) {
+        ahead_code[kKept ? j : 0] = a.in_codes[(int64_t)row * a.width + c];
+        ahead_byte[kKept ? j : 0] = a.in_scales[(int64_t)row * a.groups + c / kCkptGroup];
+      } else {
+        ahead_x[kKept ? j : 0] = static_cast<const T*>(a.x)[row * a.ldx + c];
+      }
+    }
+  };
+  auto take_any = [&](Chunk& xv, Chunk& gv) {  // columns past the width give 0
+    xv = gv = chunk_of(0.f);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (column<false>(0, j, t, threads) >= a.width) continue;
+      gv[j] = Elem<T>::to(ahead_g[j]);
+      if constexpr (CKPT)
+        xv[j] = ckpt_saturate(ckpt_value(ahead_code[kKept ? j : 0], ckpt_scale(ahead_byte[kKept ? j : 0]), kFormat), FLT_MAX);
+      else
+        xv[j] = Elem<T>::to(ahead_x[kKept ? j : 0]);
+    }
+  };
+  if (kKept) fetch_any(first);
+
   int turn = 0;
   for (int row = first; row < a.rows; row += step) {
     RawChunk<__half> numbers[CKPT && VEC ? NV : 1];  // a checkpoint's, decoded once; its scale goes into the factor of xh
+    Chunk kept_x, kept_g;
+    if (kKept) {
+      take_any(kept_x, kept_g);
+      fetch_any(row + step);
+    }
     // x and dy of a chunk that the row has; in the scalar layout, columns past the width give 0
     auto chunk = [&](int i, Chunk& xv, Chunk& gv) {
       if (VEC) {
@@ -416,7 +457,12 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
       if (!in[i]) continue;
       Chunk xv, gv;
       if (CKPT && VEC) numbers[CKPT && VEC ? i : 0] = ckpt_numbers8(*reinterpret_cast<const uint2*>(my_x + at_x + i * step_x), kFormat);
-      chunk(i, xv, gv);
+      if (kKept) {
+        xv = kept_x;
+        gv = kept_g;
+      } else {
+        chunk(i, xv, gv);
+      }
       const float2 rx = factor(i);
 #pragma unroll
       for (int j = 0; j < kChunk / 2; ++j) {
@@ -437,7 +483,12 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
       Chunk xv, gv;
-      chunk(i, xv, gv);
+      if (kKept) {
+        xv = kept_x;
+        gv = kept_g;
+      } else {
+        chunk(i, xv, gv);
+      }
       const float2 cx = both(factor(i).x * c1);
 #pragma unroll
       for (int j = 0; j < kChunk / 2; ++j)
