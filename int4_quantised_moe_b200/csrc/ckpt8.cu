@@ -30,9 +30,9 @@ __device__ __forceinline__ Place place(int64_t i, uint32_t cpr, int width, int64
 
 // Vector layout.
 template <class T, int FMT>
-__global__ void __launch_bounds__(kThreads) ckpt8_save_vec(const T* __restrict__ x, int64_t ldx, int64_t n, int width,
-                                                           uint32_t cpr, uint8_t* __restrict__ codes,
-                                                           uint8_t* __restrict__ scales, int groups) {
+__global__ void __launch_bounds__(kThreads) ckpt8_save_vec(const T* x, int64_t ldx, int64_t n, int width,
+                                                           uint32_t cpr, uint8_t* codes,
+                                                           uint8_t* scales, int groups) {
   begin_after_previous();
   const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
   RawChunk<T> r[kUnroll];
@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(kThreads) ckpt8_save_vec(const T* __restrict__
 constexpr int kAnyUnroll = 8;
 
 template <class T, int FMT>
-__global__ void __launch_bounds__(kThreads) ckpt8_save_any(const T* __restrict__ x, int64_t ldx, int64_t n, int width,
-                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+__global__ void __launch_bounds__(kThreads) ckpt8_save_any(const T* x, int64_t ldx, int64_t n, int width,
+                                                           uint8_t* codes, uint8_t* scales,
                                                            uint32_t segments, int groups) {
   begin_after_previous();
   const int lane = threadIdx.x & 31;
@@ -93,9 +93,9 @@ __global__ void __launch_bounds__(kThreads) ckpt8_save_any(const T* __restrict__
 }
 
 template <class T, int FMT>
-__global__ void __launch_bounds__(kThreads) ckpt8_load_vec(const uint8_t* __restrict__ codes,
-                                                           const uint8_t* __restrict__ scales, int64_t n, int width,
-                                                           uint32_t cpr, int groups, T* __restrict__ out) {
+__global__ void __launch_bounds__(kThreads) ckpt8_load_vec(const uint8_t* codes,
+                                                           const uint8_t* scales, int64_t n, int width,
+                                                           uint32_t cpr, int groups, T* out) {
   begin_after_previous();
   const int64_t i0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
   uint2 w[kUnroll];
@@ -125,9 +125,9 @@ __global__ void __launch_bounds__(kThreads) ckpt8_load_vec(const uint8_t* __rest
 }
 
 template <class T, int FMT>
-__global__ void __launch_bounds__(kThreads) ckpt8_load_any(const uint8_t* __restrict__ codes,
-                                                           const uint8_t* __restrict__ scales, int64_t n, int width,
-                                                           uint32_t segments, int groups, T* __restrict__ out) {
+__global__ void __launch_bounds__(kThreads) ckpt8_load_any(const uint8_t* codes,
+                                                           const uint8_t* scales, int64_t n, int width,
+                                                           uint32_t segments, int groups, T* out) {
   begin_after_previous();
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);

@@ -12,7 +12,7 @@ namespace {
 // take 0.6 us less of a backward than 16, and 2.7 less than 4.
 constexpr int kFoldWarps = 32;
 constexpr int kFoldRows = (kBwdBlocks + kFoldWarps - 1) / kFoldWarps;
-__global__ void __launch_bounds__(32 * kFoldWarps) norm_fold_kernel(const float* __restrict__ partial, int blocks,
+__global__ void __launch_bounds__(32 * kFoldWarps) norm_fold_kernel(const float* partial, int blocks,
                                                                     int width, void* gw, void* gb, int type,
                                                                     int accumulate) {
   __shared__ float sums[kFoldWarps][32];

@@ -315,6 +315,10 @@ __device__ __forceinline__ Chunk ckpt_decode8(uint2 w, uint32_t byte, int fmt) {
 // stands before a kernel's first access to memory and returns when everything
 // before it in the stream is complete and visible; it also lets the next
 // kernel's blocks take the places that this one's last blocks leave.
+// Such a kernel is resident while the one before it still writes its inputs,
+// so none of its pointers is __restrict__ and nothing is read with __ldg: both
+// say that the data stays as it is for as long as the kernel lives, and loads
+// marked so may be moved in front of the wait.
 __device__ __forceinline__ void begin_after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // after the wait: one kernel ahead, no more
