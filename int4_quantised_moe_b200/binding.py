@@ -8,7 +8,9 @@ fallback: importing this module fails loudly when the library is missing.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import warnings
 from dataclasses import dataclass
 from typing import Dict, Optional
 
@@ -151,11 +153,32 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 
-try:
-    from . import _fastcall as _fast  # csrc/fastcall.cpp
-except ImportError as e:
-    raise ImportError(f"the _fastcall extension beside {LIB_PATH} is missing or does not load ({e}): build it with "
-                      "`python -m int4_quantised_moe_b200.build`") from e
+class _NoFastcall:
+    """In the extension's place where there is none: every call is left to the code below."""
+
+    router_select = router_select_bwd = ckpt8_save = ckpt8_load = norm_fwd = norm_bwd = staticmethod(lambda *args: None)
+
+
+def _load_fastcall():
+    """The extension csrc/fastcall.cpp for this Python and torch; without it nothing is lost but the time
+    that ctypes takes on the host."""
+    from . import build
+    path = build.fastcall_path()
+    try:
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._fastcall", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError as e:
+        warnings.warn(f"the quick way into the operators around the layer does not load ({e}); their calls go through "
+                      "ctypes, some 10 us longer each. `python -m int4_quantised_moe_b200.build` builds it",
+                      RuntimeWarning, stacklevel=3)
+        return _NoFastcall
+
+
+_fast = _load_fastcall()
 
 
 def library() -> ctypes.CDLL:
@@ -489,8 +512,8 @@ def router_bwd(scores: torch.Tensor, ids: torch.Tensor, grad_route: torch.Tensor
 # the caller, as with any torch operation.
 #
 # The ordinary call (right arguments, current device and stream) is made by the
-# _fastcall extension; it answers None to every other one, which is then checked
-# and made here.
+# extension of csrc/fastcall.cpp; it answers None to every other one, which is
+# then checked and made here. Without the extension all calls are made here.
 
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}

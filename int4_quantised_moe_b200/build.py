@@ -2,7 +2,11 @@
 
 Usage: python -m int4_quantised_moe_b200.build  (or call build()).
 The library is a plain C ABI (include/rawint4_moe.h); nvcc cross-compiles it
-without a GPU.
+without a GPU. Beside it goes a small CPython extension, the quick way into the
+operators around the layer. It is compiled against the installed Python and
+torch, whose versions stand in its file name: another version finds no
+extension of its own, never a wrong one, and every call then goes through
+ctypes.
 """
 
 from __future__ import annotations
@@ -10,12 +14,12 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librawint4_moe.so")
-FASTCALL = os.path.join(HERE, "_fastcall.so")  # CPython extension over LIB: the quick way in for torch tensors
 FASTCALL_SOURCE = os.path.join(CSRC, "fastcall.cpp")
 SOURCES = ["api.cu", "gemm_pair.cu", "gemm_tm.cu", "gemm_pair_narrow.cu", "gemm_tm_narrow.cu", "skinny.cu", "route.cu",
            "aux.cu", "prof.cu", "noalloc.cu", "router.cu", "select.cu", "select_f32.cu", "select_bf16.cu",
@@ -35,12 +39,32 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(FASTCALL):
+def _older(built: str, sources) -> bool:
+    """Whether `built` is missing or older than one of its sources."""
+    if not os.path.exists(built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(FASTCALL))
-    deps = [FASTCALL_SOURCE] + [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "rawint4_moe.h")]
-    return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+    t = os.path.getmtime(built)
+    return any(os.path.getmtime(d) > t for d in sources if os.path.exists(d))
+
+
+def _header() -> str:
+    return os.path.join(ROOT, "include", "rawint4_moe.h")
+
+
+def _library_stale() -> bool:
+    return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [_header()])
+
+
+def _fastcall_stale() -> bool:
+    return _older(fastcall_path(), [FASTCALL_SOURCE, _header()])
+
+
+def fastcall_path() -> str:
+    """Where the extension for this Python and torch lies."""
+    import sysconfig
+
+    import torch
+    return os.path.join(HERE, f"_fastcall-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _build_fastcall(verbose: bool) -> None:
@@ -52,7 +76,8 @@ def _build_fastcall(verbose: bool) -> None:
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    tmp = FASTCALL + ".tmp"
+    path = fastcall_path()
+    tmp = path + ".tmp"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-isystem{p}" for p in include], FASTCALL_SOURCE, "-o", tmp, f"-L{HERE}", "-l:librawint4_moe.so",
@@ -61,12 +86,10 @@ def _build_fastcall(verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, FASTCALL)
+    os.replace(tmp, path)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
+def _build_library(verbose: bool) -> None:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     from concurrent.futures import ThreadPoolExecutor
@@ -86,7 +109,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
-    _build_fastcall(verbose)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is missing or older than its sources (force: everything). Without a host compiler or
+    torch's headers the library stands alone, with a warning."""
+    if force or _library_stale():
+        _build_library(verbose)
+    try:
+        if force or _fastcall_stale():
+            _build_fastcall(verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"the quick way into the operators around the layer was not built ({e}); their calls go "
+                      "through ctypes", RuntimeWarning)
     return LIB
 
 
