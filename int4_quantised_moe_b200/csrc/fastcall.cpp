@@ -100,6 +100,20 @@ PyObject* tuple_of(std::initializer_list<Tensor> ts) {
   return out;
 }
 
+// The interpreter's lock is let go while results are allocated and the library
+// is called: both may wait (for memory, for room in the stream's queue of
+// launches), and other threads run on meanwhile. No Python object is touched.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 PyObject* refused(int code) { return PyLong_FromLong(code); }
 
 // The selection's configuration (a ctypes structure), for scores of a type.
@@ -130,9 +144,15 @@ PyObject* router_select(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (args[2] != Py_None && !dense(here, bias = tensor(args[2]), ScalarType::Float, {cfg.experts})) Py_RETURN_NONE;
   if (args[3] != Py_None && !dense(here, counts = tensor(args[3]), ScalarType::Int, {cfg.experts})) Py_RETURN_NONE;
   const int64_t q = scores->size(0);
-  const Tensor ids = here.empty({q, cfg.top_k}, ScalarType::Long), w = here.empty({q, cfg.top_k}, ScalarType::Float);
-  const int rc = rawint4_moe_router_select(&cfg, data(scores), pitch, (int32_t)q, data<const float>(bias),
-                                           data<int64_t>(&ids), data<float>(&w), data<int32_t>(counts), here.stream());
+  Tensor ids, w;
+  int rc;
+  {
+    const Unlocked unlocked;
+    ids = here.empty({q, cfg.top_k}, ScalarType::Long);
+    w = here.empty({q, cfg.top_k}, ScalarType::Float);
+    rc = rawint4_moe_router_select(&cfg, data(scores), pitch, (int32_t)q, data<const float>(bias), data<int64_t>(&ids),
+                                   data<float>(&w), data<int32_t>(counts), here.stream());
+  }
   return rc == RAWINT4_OK ? tuple_of({ids, w}) : refused(rc);
   END_HANDLE_TH_ERRORS
 }
@@ -151,9 +171,14 @@ PyObject* router_select_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const Tensor *ids = tensor(args[2]), *grad = tensor(args[3]);
   if (!dense(here, ids, ScalarType::Long, {q, cfg.top_k}) || !dense(here, grad, ScalarType::Float, {q, cfg.top_k}))
     Py_RETURN_NONE;
-  const Tensor out = here.empty({q, cfg.experts}, scores->scalar_type());
-  const int rc = rawint4_moe_router_select_bwd(&cfg, data(scores), pitch, (int32_t)q, data<const int64_t>(ids),
-                                               data<const float>(grad), data(&out), here.stream());
+  Tensor out;
+  int rc;
+  {
+    const Unlocked unlocked;
+    out = here.empty({q, cfg.experts}, scores->scalar_type());
+    rc = rawint4_moe_router_select_bwd(&cfg, data(scores), pitch, (int32_t)q, data<const int64_t>(ids),
+                                       data<const float>(grad), data(&out), here.stream());
+  }
   return rc == RAWINT4_OK ? wrap(out) : refused(rc);
   END_HANDLE_TH_ERRORS
 }
@@ -166,10 +191,16 @@ PyObject* ckpt8_save(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const Tensor* x = n == 2 ? tensor(args[0]) : nullptr;
   if (!rows_ok(here, x, &pitch)) Py_RETURN_NONE;
   const int64_t rows = x->size(0), width = x->size(1);
-  const Tensor codes = here.empty({rows, width}, ScalarType::Byte),
-               scales = here.empty({rows, (width + kGroup - 1) / kGroup}, ScalarType::Byte);
-  const int rc = rawint4_ckpt8_save((int32_t)PyLong_AsLong(args[1]), type_of(x->scalar_type()), data(x), pitch, rows,
-                                    (int32_t)width, data<uint8_t>(&codes), data<uint8_t>(&scales), here.stream());
+  const int32_t format = (int32_t)PyLong_AsLong(args[1]);
+  Tensor codes, scales;
+  int rc;
+  {
+    const Unlocked unlocked;
+    codes = here.empty({rows, width}, ScalarType::Byte);
+    scales = here.empty({rows, (width + kGroup - 1) / kGroup}, ScalarType::Byte);
+    rc = rawint4_ckpt8_save(format, type_of(x->scalar_type()), data(x), pitch, rows, (int32_t)width,
+                            data<uint8_t>(&codes), data<uint8_t>(&scales), here.stream());
+  }
   return rc == RAWINT4_OK ? tuple_of({codes, scales}) : refused(rc);
   END_HANDLE_TH_ERRORS
 }
@@ -189,10 +220,15 @@ PyObject* ckpt8_load(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const ScalarType type = reinterpret_cast<THPDtype*>(args[3])->scalar_type;
   if (type_of(type) < 0) Py_RETURN_NONE;
   const int64_t rows = codes->size(0), width = codes->size(1);
-  const Tensor out = here.empty({rows, width}, type);
-  const int rc = rawint4_ckpt8_load((int32_t)PyLong_AsLong(args[2]), data<const uint8_t>(codes),
-                                    data<const uint8_t>(scales), rows, (int32_t)width, type_of(type), data(&out),
-                                    here.stream());
+  const int32_t format = (int32_t)PyLong_AsLong(args[2]);
+  Tensor out;
+  int rc;
+  {
+    const Unlocked unlocked;
+    out = here.empty({rows, width}, type);
+    rc = rawint4_ckpt8_load(format, data<const uint8_t>(codes), data<const uint8_t>(scales), rows, (int32_t)width,
+                            type_of(type), data(&out), here.stream());
+  }
   return rc == RAWINT4_OK ? wrap(out) : refused(rc);
   END_HANDLE_TH_ERRORS
 }
@@ -245,17 +281,22 @@ PyObject* norm_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (save >= 0 && !in.x) Py_RETURN_NONE;
   const ScalarType wtype = weight ? weight->scalar_type() : bias ? bias->scalar_type() : type;
   const rawint4_norm_cfg cfg = {(int32_t)in.rows, (int32_t)in.width, (int32_t)kind, type_of(type), type_of(wtype), (float)eps};
-  const Tensor y = here.empty({in.rows, in.width}, type), rstd = here.empty({in.rows}, ScalarType::Float);
-  Tensor mean, codes, scales;
-  if (kind == RAWINT4_NORM_LAYER) mean = here.empty({in.rows}, ScalarType::Float);
-  if (save >= 0) {
-    codes = here.empty({in.rows, in.width}, ScalarType::Byte);
-    scales = here.empty({in.rows, (in.width + kGroup - 1) / kGroup}, ScalarType::Byte);
+  Tensor y, mean, rstd, codes, scales;
+  int rc;
+  {
+    const Unlocked unlocked;
+    y = here.empty({in.rows, in.width}, type);
+    rstd = here.empty({in.rows}, ScalarType::Float);
+    if (kind == RAWINT4_NORM_LAYER) mean = here.empty({in.rows}, ScalarType::Float);
+    if (save >= 0) {
+      codes = here.empty({in.rows, in.width}, ScalarType::Byte);
+      scales = here.empty({in.rows, (in.width + kGroup - 1) / kGroup}, ScalarType::Byte);
+    }
+    rc = rawint4_norm_fwd(&cfg, data(in.x), in.pitch, in.held(), data(weight), data(bias), data(&y),
+                          mean.defined() ? data<float>(&mean) : nullptr, data<float>(&rstd),
+                          save >= 0 ? (int32_t)save : 0, save >= 0 ? data<uint8_t>(&codes) : nullptr,
+                          save >= 0 ? data<uint8_t>(&scales) : nullptr, here.stream());
   }
-  const int rc = rawint4_norm_fwd(&cfg, data(in.x), in.pitch, in.held(), data(weight), data(bias), data(&y),
-                                  mean.defined() ? data<float>(&mean) : nullptr, data<float>(&rstd),
-                                  save >= 0 ? (int32_t)save : 0, save >= 0 ? data<uint8_t>(&codes) : nullptr,
-                                  save >= 0 ? data<uint8_t>(&scales) : nullptr, here.stream());
   return rc == RAWINT4_OK ? tuple_of({y, mean, rstd, codes, scales}) : refused(rc);
   END_HANDLE_TH_ERRORS
 }
@@ -285,22 +326,25 @@ PyObject* norm_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const ScalarType wtype = weight ? weight->scalar_type() : gb_in ? gb_in->scalar_type() : type;
   if ((gw_in && gw_in->scalar_type() != wtype) || (gb_in && gb_in->scalar_type() != wtype)) Py_RETURN_NONE;
   const rawint4_norm_cfg cfg = {(int32_t)in.rows, (int32_t)in.width, (int32_t)kind, type_of(type), type_of(wtype), 1.0f};
-  const Tensor gx = here.empty({in.rows, in.width}, type);
-  Tensor gw, gb, ws;
-  if (gw_in) gw = *gw_in;
-  else if (weight) gw = here.empty({in.width}, wtype);
-  if (gb_in) gb = *gb_in;
-  else if (bias_grad) gb = here.empty({in.width}, wtype);
   size_t bytes = 0;
-  if (gw.defined() || gb.defined()) {
-    const int rc = rawint4_norm_bwd_workspace_size(&cfg, &bytes);
-    if (rc != RAWINT4_OK) return refused(rc);
-    ws = here.empty({(int64_t)bytes}, ScalarType::Byte);
+  int rc = rawint4_norm_bwd_workspace_size(&cfg, &bytes);
+  if (rc != RAWINT4_OK) return refused(rc);
+  Tensor gx, gw, gb;
+  {
+    const Unlocked unlocked;
+    Tensor ws;
+    gx = here.empty({in.rows, in.width}, type);
+    if (gw_in) gw = *gw_in;
+    else if (weight) gw = here.empty({in.width}, wtype);
+    if (gb_in) gb = *gb_in;
+    else if (bias_grad) gb = here.empty({in.width}, wtype);
+    if (gw.defined() || gb.defined()) ws = here.empty({(int64_t)bytes}, ScalarType::Byte);
+    else bytes = 0;
+    rc = rawint4_norm_bwd(&cfg, data(in.x), in.pitch, in.held(), data(gy), pitch, data(weight),
+                          mean ? data<const float>(mean) : nullptr, data<const float>(rstd), data(&gx),
+                          gw.defined() ? data(&gw) : nullptr, gb.defined() ? data(&gb) : nullptr, accumulate,
+                          ws.defined() ? data(&ws) : nullptr, bytes, here.stream());
   }
-  const int rc = rawint4_norm_bwd(&cfg, data(in.x), in.pitch, in.held(), data(gy), pitch, data(weight),
-                                  mean ? data<const float>(mean) : nullptr, data<const float>(rstd), data(&gx),
-                                  gw.defined() ? data(&gw) : nullptr, gb.defined() ? data(&gb) : nullptr, accumulate,
-                                  ws.defined() ? data(&ws) : nullptr, bytes, here.stream());
   return rc == RAWINT4_OK ? tuple_of({gx, gw, gb}) : refused(rc);
   END_HANDLE_TH_ERRORS
 }
