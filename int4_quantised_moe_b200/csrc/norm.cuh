@@ -6,8 +6,8 @@ namespace r4 {
 constexpr int kMaxWidth = 16384;
 constexpr int kFewRows = 296;        // two rows an SM
 constexpr int kFwdWarps = 8;         // rows of a forward block when a row lies in one warp
-// Threads of a backward block at most, so that w, dw and db (8 registers a
-// chunk each) fit: 128, 96 and 72 registers a thread.
+// Threads of a backward block at most: 128, 96 and 72 registers a thread
+// beside w, dw and db (8 a chunk each).
 __host__ __device__ constexpr int bwd_threads(int nv) { return nv == 4 ? 512 : nv == 2 ? 640 : 896; }
 constexpr int kBwdBlocks = 148;      // blocks of the backward at most, one an SM: rows of partial sums
 constexpr int kBwdMaxStages = 4;     // rows in a thread group's ring

@@ -9,7 +9,15 @@
 //
 // Forward: a row lies in the registers of one warp (narrow rows, several rows
 // a block) or of one block, so the input is read once: the mean, then the
-// centred squares, are summed from registers in fp32.
+// centred squares, are summed from registers in fp32. The sum over a row's bf16
+// values or a checkpoint's (8 bits each) is exact where they are of one size, and
+// so is the mean. With more bits (fp32, fp16) the centred values are summed along
+// with their squares, and what their mean lacks of 0 corrects the mean. A row of
+// one value has that value for its mean in either case.
+//
+// xh is formed as (x - mu) r in both directions. x r - mu r would save an
+// instruction a pair, but the rounding of mu r stays when x - mu is small: rows of
+// the value 5 would get 2e-4 in place of 0.
 //
 // Backward: a fixed grid of blocks walks the rows. The threads of a row copy
 // their own chunks of the coming rows into shared memory (cp.async, a ring of
@@ -18,6 +26,8 @@
 // registers; each block writes one partial row of sums, and a second kernel
 // adds the partials in block order, so the result does not depend on timing.
 #pragma once
+#include <type_traits>
+
 #include "norm.cuh"
 
 namespace r4 {
@@ -144,9 +154,11 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int threads, int ba
 // with a scale a chunk), else as fp32.
 template <class T, class R, int NV, bool VEC, int CKPT>
 __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormArgs a) {
-  __shared__ float buf[2][16];
+  __shared__ float buf[16];
+  __shared__ float2 buf2[16];
   constexpr bool kScaled = VEC && CKPT;
   constexpr int kFormat = CKPT - 1;
+  constexpr bool kCorrect = !kScaled && !std::is_same<R, __nv_bfloat16>::value;
   begin_after_previous();
   const int t = threadIdx.x, threads = blockDim.x;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
@@ -192,7 +204,13 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
 
   const float inv_n = 1.0f / (float)a.width;
   float mu = 0.f;
+  // x - mu of pair j of chunk i
+  auto centred = [&](float2 x, int i) {
+    if constexpr (kScaled) return fma2(x, both(scale[i]), both(-mu));
+    else return add2(x, both(-mu));
+  };
   float2 q = both(0.f);
+  float var;
   if (a.layer) {
     float2 s = both(0.f);
 #pragma unroll
@@ -201,20 +219,34 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
 #pragma unroll
       for (int j = 0; j < kChunk / 2; ++j) s = kScaled ? fma2(v.p[j], both(scale[kScaled ? i : 0]), s) : add2(s, v.p[j]);
     }
-    mu = row_sum(s.x + s.y, threads, 1, buf[0]) * inv_n;
+    const float total = row_sum(s.x + s.y, threads, 1, buf);
+    mu = total * inv_n;
+    mu = fmaf(fmaf(-mu, (float)a.width, total), inv_n, mu);  // the quotient, to its last bit if it ends there
+    s = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
       Chunk d = widen<R>(x[i]);
 #pragma unroll
-      for (int j = 0; j < kChunk / 2; ++j)
-        d.p[j] = kScaled ? fma2(d.p[j], both(scale[kScaled ? i : 0]), both(-mu)) : add2(d.p[j], both(-mu));
+      for (int j = 0; j < kChunk / 2; ++j) d.p[j] = centred(d.p[j], i);
       if (!VEC)
 #pragma unroll
         for (int j = 0; j < kChunk; ++j)
           if (column<false>(i, j, t, threads) >= a.width) d[j] = 0.f;
 #pragma unroll
-      for (int j = 0; j < kChunk / 2; ++j) q = fma2(d.p[j], d.p[j], q);
+      for (int j = 0; j < kChunk / 2; ++j) {
+        if (kCorrect) s = add2(s, d.p[j]);
+        q = fma2(d.p[j], d.p[j], q);
+      }
+    }
+    if constexpr (kCorrect) {
+      const float2 sums = row_sum2(s.x + s.y, q.x + q.y, threads, 1, buf2);
+      const float shift = sums.x * inv_n;
+      mu += shift;
+      var = fmaxf(sums.y * inv_n - shift * shift, 0.f);
+      if (!(sums.y < INFINITY)) var = sums.y;  // infinities and NaN stay what they are
+    } else {
+      var = row_sum(q.x + q.y, threads, 1, reinterpret_cast<float*>(buf2)) * inv_n;
     }
   } else {
 #pragma unroll
@@ -225,9 +257,9 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
       for (int j = 0; j < kChunk / 2; ++j) s = fma2(v.p[j], v.p[j], s);
       q = kScaled ? fma2(mul2(s, both(scale[kScaled ? i : 0])), both(scale[kScaled ? i : 0]), q) : s;
     }
+    var = row_sum(q.x + q.y, threads, 1, buf) * inv_n;
   }
-  const float r = 1.0f / sqrtf(row_sum(q.x + q.y, threads, 1, buf[1]) * inv_n + a.eps);
-  const float2 off = both(-mu * r);
+  const float r = 1.0f / sqrtf(var + a.eps);
   T* const y = static_cast<T*>(a.y) + (int64_t)row * a.width;
   // y of chunk i, given the weight's and bias's tensor type
   auto finish = [&](auto wt) {
@@ -238,9 +270,14 @@ __global__ void __launch_bounds__(512, VEC ? 2 : 1) norm_fwd_kernel(const NormAr
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
       Chunk v = widen<R>(x[i]);
-      const float2 rx = both(kScaled ? r * scale[kScaled ? i : 0] : r);
+      if (a.layer) {
 #pragma unroll
-      for (int j = 0; j < kChunk / 2; ++j) v.p[j] = fma2(v.p[j], rx, off);
+        for (int j = 0; j < kChunk / 2; ++j) v.p[j] = mul2(centred(v.p[j], i), both(r));
+      } else {
+        const float2 rx = both(kScaled ? r * scale[kScaled ? i : 0] : r);
+#pragma unroll
+        for (int j = 0; j < kChunk / 2; ++j) v.p[j] = mul2(v.p[j], rx);
+      }
       if (w) {
         const Chunk f = VEC ? widen<W>(load_chunk(w + t * kChunk + i * stride)) : any_chunk(w, i, t, threads, a.width);
 #pragma unroll
@@ -384,7 +421,9 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
   fetch_stats(first);
   T* out = static_cast<T*>(a.gx) + (int64_t)first * a.width;
 
-  // the scalar layout with one chunk a thread: the next row's elements, as they come, wait in registers
+  // the scalar layout with one chunk a thread: the next row's elements, as they come, wait in registers. They are
+  // asked for at once, or behind the row's sums where db leaves too few registers (loads on their way would be
+  // spilled and waited for: 4096 x 3329 bf16 layer norm with db 41 us, asked for at once 63)
   constexpr bool kKept = !VEC && NV == 1;
   constexpr int kAhead = kKept ? kChunk : 1, kAheadX = kKept && !CKPT ? kChunk : 1, kAheadC = kKept && CKPT ? kChunk : 1;
   T ahead_g[kAhead], ahead_x[kAheadX];
@@ -405,7 +444,7 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
       }
     }
   };
-  auto take_any = [&](Chunk& xv, Chunk& gv) {  // columns past the width give 0
+  auto take_any = [&](Chunk& xv, Chunk& gv, float mean) {  // x - mean and dy; columns past the width give 0
     xv = gv = chunk_of(0.f);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -415,6 +454,7 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
         xv[j] = ckpt_saturate(ckpt_value(ahead_code[kKept ? j : 0], ckpt_scale(ahead_byte[kKept ? j : 0]), kFormat), FLT_MAX);
       else
         xv[j] = Elem<T>::to(ahead_x[kKept ? j : 0]);
+      if (LAYER) xv[j] -= mean;
     }
   };
   if (kKept) fetch_any(first);
@@ -424,8 +464,8 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
     RawChunk<__half> numbers[CKPT && VEC ? NV : 1];  // a checkpoint's, decoded once; its scale goes into the factor of xh
     Chunk kept_x, kept_g;
     if (kKept) {
-      take_any(kept_x, kept_g);
-      fetch_any(row + step);
+      take_any(kept_x, kept_g, next_mu);
+      if (!SUMB) fetch_any(row + step);
     }
     // x and dy of a chunk that the row has; in the scalar layout, columns past the width give 0
     auto chunk = [&](int i, Chunk& xv, Chunk& gv) {
@@ -449,9 +489,28 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
     fetch_stats(row + step);
     if (VEC) copy_wait_but(a.stages - 1);
 
+    // in the scalar layout not as pairs, which want their factors twice in neighbouring registers
+    auto mul = [](float2 a, float2 b) {
+      if constexpr (VEC) return mul2(a, b);
+      else return make_float2(a.x * b.x, a.y * b.y);
+    };
+    auto add = [](float2 a, float2 b) {
+      if constexpr (VEC) return add2(a, b);
+      else return make_float2(a.x + b.x, a.y + b.y);
+    };
+    auto fma = [](float2 a, float2 b, float2 c) {
+      if constexpr (VEC) return fma2(a, b, c);
+      else return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+    };
     float2 s1 = both(0.f), s2 = both(0.f);
-    const float2 r2 = both(r), off = both(-mu * r);
-    auto factor = [&](int i) { return CKPT && VEC ? both(r * ckpt_scale(bytes[i])) : r2; };
+    constexpr bool kLate = LAYER || !(CKPT && VEC);
+    const float2 r2 = both(r), minus_mu = both(-mu);
+    // factor(i) times off_mean(x, i) is xh
+    auto off_mean = [&](float2 x, int i) {
+      if (!LAYER || kKept) return x;
+      return CKPT && VEC ? fma(x, both(ckpt_scale(bytes[i])), minus_mu) : add(x, minus_mu);
+    };
+    auto factor = [&](int i) { return CKPT && VEC && !LAYER ? both(r * ckpt_scale(bytes[i])) : r2; };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
@@ -466,19 +525,27 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
       const float2 rx = factor(i);
 #pragma unroll
       for (int j = 0; j < kChunk / 2; ++j) {
-        const float2 gx = mul2(gv.p[j], fma2(xv.p[j], rx, off));  // dy xh
-        dw[i].p[j] = add2(dw[i].p[j], gx);
-        s2 = fma2(gx, w[i].p[j], s2);
-        if (SUMB) db[i].p[j] = add2(db[i].p[j], gv.p[j]);
-        if (LAYER) s1 = fma2(gv.p[j], w[i].p[j], s1);
+        if (kLate) {  // dy (x - mu): r comes in with dw's sum and, for the row, behind its sum
+          const float2 gx = mul(gv.p[j], off_mean(xv.p[j], i));
+          dw[i].p[j] = fma(gx, r2, dw[i].p[j]);
+          s2 = fma(gx, w[i].p[j], s2);
+        } else {  // a checkpoint's scales differ within the row: dy xh
+          const float2 gx = mul(gv.p[j], mul(xv.p[j], rx));
+          dw[i].p[j] = add(dw[i].p[j], gx);
+          s2 = fma(gx, w[i].p[j], s2);
+        }
+        if (SUMB) db[i].p[j] = add(db[i].p[j], gv.p[j]);
+        if (LAYER) s1 = fma(gv.p[j], w[i].p[j], s1);
       }
     }
     float2 s;
     if (LAYER) s = row_sum2(s1.x + s1.y, s2.x + s2.y, threads, 1 + group, buf[turn] + warp0);
     else s = make_float2(0.f, row_sum(s2.x + s2.y, threads, 1 + group, reinterpret_cast<float*>(buf[turn] + warp0)));
-    // dx = r w dy + x c1 r + c0, from dx = r (w dy - m1 - xh m2) with xh = x r - mu r
+    if (kKept && SUMB) fetch_any(row + step);
+    // dx = r w dy + xh c1 + c0, from dx = r (w dy - m1 - xh m2)
+    if (kLate) s.y *= r;
     const float c1 = -r * (s.y * inv_n);
-    const float2 c0 = both(-(mu * r) * c1 - r * (s.x * inv_n));
+    const float2 c0 = both(-r * (s.x * inv_n));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
@@ -492,7 +559,7 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
       const float2 cx = both(factor(i).x * c1);
 #pragma unroll
       for (int j = 0; j < kChunk / 2; ++j)
-        xv.p[j] = fma2(mul2(gv.p[j], w[i].p[j]), r2, fma2(xv.p[j], cx, c0));
+        xv.p[j] = fma(mul(gv.p[j], w[i].p[j]), r2, LAYER ? fma(off_mean(xv.p[j], i), cx, c0) : mul(xv.p[j], cx));
       if (VEC) store_chunk(out + t * kChunk + i * stride, xv);
       else store_any_chunk(out, i, t, threads, a.width, xv);
     }
