@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(32 * kWarps, NI <= 4 ? 2 : 1) select_kernel(co
     if (a.renorm) {
       float total;
       const float q = slot_share(v, a.sigmoid, &total);
-      w = total > 0.f ? a.scale * __fdividef(q, total) : 0.f;
+      w = total > 0.f ? a.scale * (q / total) : 0.f;
     } else {
       w = v > -INFINITY ? a.scale * (a.sigmoid ? 1.f / (1.f + expf(-v)) : shifted_exp(v, m) / denom) : 0.f;
     }
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) select_many_kernel(const Selec
       if (v > -INFINITY)
         w = a.sigmoid ? expf(fminf(v, 0.f) - fminf(m, 0.f)) / (1.f + expf(-fabsf(v))) : shifted_exp(v, m);
       const float total = part_sum<8>(w);
-      w = total > 0.f ? a.scale * __fdividef(w, total) : 0.f;
+      w = total > 0.f ? a.scale * (w / total) : 0.f;
     } else if (a.sigmoid) {
       w = v > -INFINITY ? a.scale / (1.f + expf(-v)) : 0.f;
     } else {
