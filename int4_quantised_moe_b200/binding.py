@@ -387,6 +387,7 @@ class Layer:
     lora: Lora
     workspace: torch.Tensor
     keep: tuple  # tensors whose pointers live in base/lora
+    passes: int = 0  # forwards and backwards so far: each replaces or consumes the saved context
 
     @classmethod
     def create(cls, experts, top_k, hidden, inter, rank, alpha, swiglu_limit, max_tokens, gate_q, gate_s, up_q, up_s,
@@ -424,6 +425,7 @@ class Layer:
         if out is None:
             out = torch.empty_like(x)
         _expect(out, "out", torch.bfloat16, (q, H), dev)
+        self.passes += 1
         rawint4_moe_lora_fwd(self.cfg, self.base, self.lora if use_lora else None, q, expert_ids, route_weights, x,
                              out, save_for_backward, self.workspace, stream)
         return out
@@ -443,6 +445,7 @@ class Layer:
             if name not in grads:
                 raise KeyError(f"grads: missing {name}")
             _expect(grads[name], f"grads[{name}]", torch.bfloat16, shape, dev)
+        self.passes += 1
         rawint4_moe_lora_bwd(self.cfg, self.base, self.lora, grad_out, grad_in, grad_route, make_grads(grads),
                              accumulate, grad_scale, self.workspace, stream, **base_grads)
         return grad_in

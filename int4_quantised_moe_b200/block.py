@@ -18,7 +18,10 @@ again, repeats the layer's forward for the experts chosen before, and goes
 back from there. Blocks that train one after another may then share a layer
 workspace. Gradients are those of the kept values: the norm's statistics, h and
 the layer's context are formed anew from the checkpoint, the selection is not.
-With ``keep=None`` x and the layer's saved context stay as they are.
+With ``keep=None`` x and the layer's saved context stay as they are: x may not
+be written to before ``finish``, and a forward or backward on the same layer
+before this block's ``backward`` would replace the context, so that ``backward``
+is refused then.
 
 `layer` is a ``binding.Layer`` or an ``ep.ExpertParallelLayer``.
 """
@@ -56,6 +59,7 @@ class RoutedBlock:
         self._x = None      # x, or its checkpoint
         self._stats = None  # (mean, rstd) of what is kept
         self._route = None  # (scores, ids, weights)
+        self._passes = 0    # of the layer, when its context was this block's (keep=None)
         self._stage = "normalise"  # the call that comes next
 
     def _expects(self, call: str) -> None:
@@ -80,6 +84,7 @@ class RoutedBlock:
         out = self.layer.forward(ids, weights, h, save_for_backward=train and self.keep is None)
         if train:
             self._route = (scores, ids, weights)
+            self._passes = self.layer.passes
             self._stage = "backward"
         else:
             self._x = self._stats = None
@@ -90,6 +95,9 @@ class RoutedBlock:
                  grad_scale: float = 1.0):
         """(grad_h [Q, H] through the layer, grad_scores [Q, E]); fills the layer's LoRA gradients."""
         self._expects("backward")
+        if self.keep is None and self.layer.passes != self._passes:
+            raise RuntimeError("the layer's saved context is no longer this pass's: another forward or backward ran on the "
+                               "layer (blocks that share one need keep=\"e4m3\" or \"int8\")")
         scores, ids, weights = self._route
         if self.keep is not None:
             h, mean, rstd, _ = B.norm_fwd(self._x, self.norm_weight, self.norm_bias, kind=self.kind, eps=self.eps,

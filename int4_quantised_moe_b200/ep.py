@@ -102,6 +102,7 @@ class ExpertParallelLayer:
         self.capacity = capacity
         self.ops = ops or library_ops()
         self._ctx = None
+        self.passes = 0  # forwards and backwards so far, as in binding.Layer
 
     # ------------------------------------------------------------------ plan
     def _plan(self, expert_ids: torch.Tensor):
@@ -126,6 +127,7 @@ class ExpertParallelLayer:
         if k != self.top_k:
             raise ValueError(f"expert_ids has {k} slots per token, the layer top_k is {self.top_k}")
         h = x.shape[1]
+        self.passes += 1
         perm, inv, send, recv = self._plan(expert_ids)
         n_send, n_recv = int(sum(send)), int(sum(recv))
         if n_recv > self.capacity:
@@ -155,6 +157,7 @@ class ExpertParallelLayer:
         with the gradient-window semantics of the single-process layer."""
         if self._ctx is None:
             raise RuntimeError("backward without a saved forward")
+        self.passes += 1
         perm, inv, send, recv, q, k, h = self._ctx
         self._ctx = None
         n_send, n_recv = int(sum(send)), int(sum(recv))
