@@ -117,6 +117,8 @@ class RoutedBlock:
         plus the router projection's; ends the pass."""
         self._expects("finish")
         mean, rstd = self._stats
+        if self.norm_bias is not None and self.norm_weight is None and grad_bias is None and not accumulate:
+            grad_bias = torch.empty_like(self.norm_bias)  # without a weight, norm_bwd would take grad_h's type
         out = B.norm_bwd(grad_h, self._x, rstd, self.norm_weight, mean=mean, kind=self.kind,
                          bias_grad=self.norm_bias is not None, grad_weight=grad_weight, grad_bias=grad_bias,
                          accumulate=accumulate)

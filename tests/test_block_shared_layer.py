@@ -128,3 +128,30 @@ def test_shared_layer_on_the_device():
             if got is not None:
                 assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert layer.status() == 0
+
+
+def test_gradient_of_a_bias_without_weight_has_its_type(plain, monkeypatch):
+    """norm_bwd cannot see the bias; the block asks for the gradient in its type."""
+    seen = {}
+    monkeypatch.setattr(block_module.B, "norm_bwd", lambda g, *a, **kw: (seen.update(kw), (g, None, kw["grad_bias"]))[1])
+    bias = torch.zeros(4, dtype=torch.float16)
+    block = RoutedBlock(CountingLayer(), B.make_select_cfg(4, 1), norm_bias=bias, kind="layer", keep=None)
+    begin(block)
+    block.backward(torch.zeros(2, 4), {})
+    _, _, grad_bias = block.finish(torch.zeros(2, 4))
+    assert seen["bias_grad"] and grad_bias.dtype == torch.float16 and grad_bias.shape == (4,)
+
+
+@pytest.mark.gpu
+def test_gradient_of_a_bias_without_weight_on_the_device():
+    from tests._gpu import grad_buffers, make_layer
+    cfg = small_config("block", experts=8, top_k=2, hidden=256, inter=128, rank=8, qlen=67)
+    wl = make_workload(cfg)
+    dev = wl.to("cuda")
+    block = RoutedBlock(make_layer(dev), B.make_select_cfg(8, 2), norm_bias=torch.zeros(256, device="cuda"), kind="layer")
+    block.forward(block.normalise(dev.x), torch.randn((67, 8), generator=torch.Generator().manual_seed(4)).cuda())
+    gh, _ = block.backward(dev.grad_out, grad_buffers(wl))
+    _, grad_weight, grad_bias = block.finish(gh)
+    assert grad_weight is None and grad_bias.dtype == torch.float32
+    want = gh.double().sum(0)  # 67 terms and the fold, each addition rounded in fp32
+    assert ((grad_bias.double() - want).abs() <= 256 * 2.0 ** -24 * gh.double().abs().sum(0)).all()
