@@ -601,15 +601,17 @@ __global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArg
 // ------------------------------------------------------------- launch shapes
 // Forward: eight chunks of a 16-bit row a thread keep a block's warps, and the
 // time they wait for one another, few (8192 x 7168 bf16 RMS: 38 us, with four
-// 45); with a mean (layer norm with bias: 63 us, with four 50) or a checkpoint's
-// numbers (4096 x 2816 from INT8: 16 us, with four 11) eight do not fit the
-// registers. Few rows want many threads each (1 x 7168: eight chunks 3.8 us,
-// four 3.0, two 2.5).
+// 45); with a mean (layer norm with bias: 65 us, with four 52) or a checkpoint's
+// numbers eight do not fit the registers, so four (4096 x 2816 from INT8: 11.3 us,
+// with two 13.0). Few rows want many threads each (1 x 7168: eight chunks 3.8 us,
+// four 2.9, two 2.4).
 Shape fwd_shape(const NormArgs& a, int type) {
   if (!a.vec) {
-    // scalar layout: few elements a thread (8192 x 2817 bf16: eight 57 us, sixteen 94)
-    const Shape s = shape_for(a.width, 1, a.rows <= kFewRows ? 1 : kFwdWarps);
-    return s.threads <= 512 ? s : shape_for(a.width, a.width <= 2 * kChunk * 512 ? 2 : 4, 1);
+    // scalar layout: two chunks a thread (8192 x 2817 bf16 RMS: one 44 us, two 33, four 37; 4096 x 8191: two 60, four
+    // 63), one where rows are few (400 x 2817: one 3.5 us, two 3.9); a block has at most 512 threads
+    int most = a.rows <= kFewRows ? 1 : 2;
+    while (a.width > most * kChunk * 512) most *= 2;
+    return shape_for(a.width, most, a.rows <= kFewRows ? 1 : kFwdWarps);
   }
   int most = !a.in_codes && type != RAWINT4_TYPE_F32 && !a.layer ? 8 : 4;
   if (a.rows <= kFewRows && a.width <= 2 * kChunk * 512) most = 2;
