@@ -327,8 +327,13 @@ __device__ __forceinline__ void copy_wait_but(int n) {
 // dx; otherwise they are read from memory (a row ahead into registers where a
 // thread has one chunk, else twice, the second time from cache).
 // The scale bytes of a checkpoint are fetched one row ahead into registers.
+// One block an SM runs, and the bounds say so: left open, four chunks from E4M3
+// with db and a mean were compiled for two, at 64 registers and 956 bytes of
+// spills a thread (4096 x 12288: 270 us, now 146; RMS of 4096 x 9001: 165, now
+// 131). Not so the vector layout's plain RMS, which loses its place for the four
+// chunks' numbers by it (8192 x 7168 from E4M3: 69 us, with the bound 85).
 template <class T, int NV, bool VEC, int CKPT, bool SUMB, bool LAYER>
-__global__ void __launch_bounds__(bwd_threads(NV)) norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(bwd_threads(NV), VEC && !SUMB && !LAYER ? 0 : 1) norm_bwd_kernel(const NormArgs a) {
   __shared__ float2 buf[2][32];
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kFormat = CKPT - 1;
