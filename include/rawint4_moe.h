@@ -343,8 +343,9 @@ enum { RAWINT4_TYPE_F32 = 0, RAWINT4_TYPE_BF16 = 1, RAWINT4_TYPE_F16 = 2 }; /* e
  * largest keys (experts scored -inf are left out unless nothing else remains),
  * and only the groups_kept groups of largest score stay in. The top_k experts
  * of largest key are selected, largest first; equal keys, and equal groups, go
- * to the lower index. Keys are compared as the real numbers they stand for,
- * not as their fp32 roundings. weights = scale * p_i / (sum of the k p) when
+ * to the lower index. Without a bias the scores themselves are compared; keys
+ * with a bias, and sums of two keys, as their values in double, not as their
+ * fp32 roundings. weights = scale * p_i / (sum of the k p) when
  * renormalise is nonzero, else scale * p_i; the bias only ranks.
  * A score of -inf or NaN has p = 0 and ranks behind every other score: a token
  * with fewer than k other scores gets the lowest such indices with weight 0. A

@@ -6,8 +6,11 @@ namespace r4 {
 constexpr int kMaxWidth = 16384;
 constexpr int kFewRows = 296;        // two rows an SM
 constexpr int kFwdWarps = 8;         // rows of a forward block when a row lies in one warp
-// Threads of a backward block at most: 128, 96 and 72 registers a thread
-// beside w, dw and db (8 a chunk each).
+// Threads of a backward block at most: 128, 96 and 72 registers a thread. w, dw
+// and db take 8 a chunk each. Spills in bytes a thread, vector layout: none to 24
+// without db; with it none at one chunk, up to 48 at two, 12 to 84 at four from a
+// tensor and 156 to 300 from a checkpoint. Scalar layout, whose next row waits in
+// registers too: none to 88 without db, up to 108, 60 and 240 with it.
 __host__ __device__ constexpr int bwd_threads(int nv) { return nv == 4 ? 512 : nv == 2 ? 640 : 896; }
 constexpr int kBwdBlocks = 148;      // blocks of the backward at most, one an SM: rows of partial sums
 constexpr int kBwdMaxStages = 4;     // rows in a thread group's ring
@@ -62,10 +65,10 @@ inline Shape shape_for(int width, int most, int warps_rows) {
 
 // Backward: four chunks a thread, fewer where db needs registers too: two, or
 // one next to a checkpoint's numbers, if the row's threads then fit a block
-// (8192 x 7168 bf16 RMS: four 62 us, two 78; 4095 x 704 fp32 with db: two
-// 13.7 us, one 14.8; 4096 x 2816 from INT8 with db: four 37 us, two 27.5, one 25).
-// The scalar layout takes one, the next row's elements waiting beside it
-// (8192 x 2817 bf16 RMS: four 75 us, one 61).
+// (with the fold, 8192 x 7168 bf16 RMS: four 61 us, two 70; 4095 x 704 fp32 with
+// db: two 13.3 us, one 14.2; 4096 x 2816 bf16 with db: four 26 us, two 21, from
+// INT8: four 36, two 26, one 24). The scalar layout takes one, the next row's
+// elements waiting beside it (8192 x 2817 bf16 RMS: four 106 us, two 102, one 54).
 inline Shape bwd_shape(const NormArgs& a) {
   int most = !a.vec ? 1 : !a.want_b ? 4 : a.in_codes ? 1 : 2;
   Shape s = shape_for(a.width, most, 1);

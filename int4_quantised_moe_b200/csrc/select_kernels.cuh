@@ -13,8 +13,10 @@
 // with an error bound. Where the gaps between the best keys exceed the bound
 // the selection stands; experts or groups whose order is open (about one token
 // in a hundred has some) are ordered again by their keys in double. Tokens that
-// the fp32 form cannot hold (too few scores left, keys out of range) are
-// selected in double as a whole.
+// the fp32 form cannot hold (too few scores left, keys out of range, more than
+// 31 candidates of open order) are selected in double as a whole. That is slow
+// where it is every token: 8192 x 384 fp32 sigmoid with a bias takes 14 us, with
+// four scores left a token 42, with equal keys everywhere (a router's start) 64.
 //
 // One warp a token, scores in registers, four neighbours a lane and step. A
 // key becomes one 32-bit number: its place in the range of possible keys (23
@@ -786,7 +788,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) select_many_kernel(const Selec
   }
 }
 
-// Rows of more than 1024 experts: the keys lie in shared memory, in double.
+// Rows of more than 1024 experts: the keys lie in shared memory, in double, and
+// every round of the top-k looks at all of them (8192 x 1025 fp32 with a bias
+// 117 us, x 4096 1140; 1024 experts in registers take 26). Built to be right, not
+// to be quick.
 template <class T>
 __global__ void __launch_bounds__(32 * kWarps) select_wide_kernel(const SelectArgs a) {
   begin_after_previous();
