@@ -425,9 +425,9 @@ class Layer:
         if out is None:
             out = torch.empty_like(x)
         _expect(out, "out", torch.bfloat16, (q, H), dev)
-        self.passes += 1
         rawint4_moe_lora_fwd(self.cfg, self.base, self.lora if use_lora else None, q, expert_ids, route_weights, x,
                              out, save_for_backward, self.workspace, stream)
+        self.passes += 1  # a refused call leaves the context as it was
         return out
 
     def backward(self, grad_out, grads: Dict[str, torch.Tensor], accumulate=False, grad_scale=1.0, grad_in=None,
@@ -445,9 +445,9 @@ class Layer:
             if name not in grads:
                 raise KeyError(f"grads: missing {name}")
             _expect(grads[name], f"grads[{name}]", torch.bfloat16, shape, dev)
-        self.passes += 1
         rawint4_moe_lora_bwd(self.cfg, self.base, self.lora, grad_out, grad_in, grad_route, make_grads(grads),
                              accumulate, grad_scale, self.workspace, stream, **base_grads)
+        self.passes += 1
         return grad_in
 
     def status(self, stream=None) -> int:

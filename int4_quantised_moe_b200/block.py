@@ -84,7 +84,7 @@ class RoutedBlock:
         out = self.layer.forward(ids, weights, h, save_for_backward=train and self.keep is None)
         if train:
             self._route = (scores, ids, weights)
-            self._passes = self.layer.passes
+            self._passes = getattr(self.layer, "passes", None)  # a layer of the caller's own need not count
             self._stage = "backward"
         else:
             self._x = self._stats = None
@@ -95,7 +95,7 @@ class RoutedBlock:
                  grad_scale: float = 1.0):
         """(grad_h [Q, H] through the layer, grad_scores [Q, E]); fills the layer's LoRA gradients."""
         self._expects("backward")
-        if self.keep is None and self.layer.passes != self._passes:
+        if self.keep is None and getattr(self.layer, "passes", None) != self._passes:
             raise RuntimeError("the layer's saved context is no longer this pass's: another forward or backward ran on the "
                                "layer (blocks that share one need keep=\"e4m3\" or \"int8\")")
         scores, ids, weights = self._route

@@ -127,7 +127,6 @@ class ExpertParallelLayer:
         if k != self.top_k:
             raise ValueError(f"expert_ids has {k} slots per token, the layer top_k is {self.top_k}")
         h = x.shape[1]
-        self.passes += 1
         perm, inv, send, recv = self._plan(expert_ids)
         n_send, n_recv = int(sum(send)), int(sum(recv))
         if n_recv > self.capacity:
@@ -143,6 +142,7 @@ class ExpertParallelLayer:
         w_recv = _exchange(self.dist, weights, send, recv)
         y_recv = self.local.forward(ids_recv.view(-1, 1), w_recv.view(-1, 1), x_recv,
                                     save_for_backward=save_for_backward)
+        self.passes += 1
         y_send = _exchange(self.dist, y_recv, recv, send)
         out = torch.empty((q, h), dtype=torch.bfloat16, device=x.device)
         self.ops.combine_slots(y_send, inv, q, k, out)

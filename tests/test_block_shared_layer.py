@@ -8,7 +8,7 @@ from int4_quantised_moe_b200 import binding as B
 from int4_quantised_moe_b200 import block as block_module
 from int4_quantised_moe_b200.block import RoutedBlock
 from int4_quantised_moe_b200.ep import ExpertParallelLayer
-from workloads import make_workload, small_config
+from workloads import lora_shapes, make_workload, small_config
 
 
 class CountingLayer:
@@ -82,6 +82,44 @@ def test_blocks_that_keep_their_input_share(plain):
     begin(second)
     end(first)
     end(second)
+
+
+def test_a_layer_that_does_not_count(plain):
+    """A wrapper with forward and backward alone works as before; nothing is checked."""
+    layer = CountingLayer()
+
+    class Wrapper:
+        def forward(self, *args, **kw):
+            return layer.forward(*args, **kw)
+
+        def backward(self, *args, **kw):
+            return layer.backward(*args, **kw)
+
+    block, = blocks(Wrapper(), None)
+    begin(block)
+    end(block)
+
+
+def test_a_refused_call_does_not_count(monkeypatch):
+    """The library refuses before it touches the workspace, so the saved context is still there."""
+    wl = make_workload(small_config("block", experts=2, top_k=1, hidden=64, inter=64, rank=8, qlen=3))
+    monkeypatch.setattr(B, "_expect", lambda *args: None)  # host tensors; the calls are replaced
+    monkeypatch.setattr(B, "make_grads", lambda grads: None)
+    layer = B.Layer(B.make_cfg(2, 1, 64, 64, 8, 16.0, 0.0, 3), None, None, torch.zeros(256, dtype=torch.uint8), ())
+
+    def refuse(*args, **kw):
+        raise B.RawInt4Error(B.INVALID_ARGUMENT, "refused")
+
+    grads = {n: torch.zeros(s, dtype=torch.bfloat16) for n, s in lora_shapes(wl.cfg).items()}
+    for fwd, bwd, counted in ((refuse, refuse, 0), (lambda *a, **k: None, refuse, 1), (lambda *a, **k: None, lambda *a, **k: None, 3)):
+        monkeypatch.setattr(B, "rawint4_moe_lora_fwd", fwd)
+        monkeypatch.setattr(B, "rawint4_moe_lora_bwd", bwd)
+        for call in (lambda: layer.forward(wl.expert_ids, wl.route_weights, wl.x), lambda: layer.backward(wl.grad_out, grads)):
+            try:
+                call()
+            except B.RawInt4Error:
+                pass
+        assert layer.passes == counted
 
 
 def test_expert_parallel_layers_count_too():
