@@ -402,7 +402,8 @@ RAWINT4_API int rawint4_ckpt8_load(int32_t format, const uint8_t* codes, const u
 
 /* Layer norm and RMS norm of rows: with mu the row mean (RMS: 0) and
  * r = 1 / sqrt(mean((x - mu)^2) + eps), y = (x - mu) r w + b. Statistics and
- * sums in fp32, each output rounded once.
+ * sums in fp32, each output rounded once; a row's sums of (x - mu)^2 and, in the
+ * backward, of dy w (x - mu) have to stay in fp32's range.
  * Limits: 1 <= width <= 16384, 0 <= rows <= 2^30, eps > 0 and finite. */
 enum { RAWINT4_NORM_LAYER = 0, RAWINT4_NORM_RMS = 1 };
 typedef struct rawint4_norm_cfg {
